@@ -12,6 +12,6 @@ from .ops import (  # noqa: F401
     Layout, alloc_layout, combine, grouped_down, grouped_gate_up, grouped_gate_up_gather,
     grouped_swiglu, layout,
     layout_desc, layout_m_cap, layout_workspace_bytes, pack_weights, permute, route,
-    validate_layout,
+    route_scored, route_scored_backward, validate_layout,
 )
 from .layer import MoELayer  # noqa: F401

@@ -28,6 +28,12 @@ class LayoutDesc(C.Structure):
                 ("ep_size", C.c_int32), ("local_rank", C.c_int32), ("align", C.c_int32)]
 
 
+class RouteDesc(C.Structure):
+    _fields_ = [("num_tokens", C.c_int64), ("num_experts", C.c_int32), ("top_k", C.c_int32),
+                ("score", C.c_int32), ("num_groups", C.c_int32), ("top_groups", C.c_int32),
+                ("group_rank", C.c_int32), ("renormalise", C.c_int32), ("scale", C.c_float)]
+
+
 _P = C.c_void_p
 _I32, _I64, _SZ = C.c_int32, C.c_int64, C.c_size_t
 
@@ -36,6 +42,8 @@ SIGNATURES = {
     "moe_status_string": (C.c_char_p, [_I32]),
     "moe_abi_version": (_I32, []),
     "moe_route": (_I32, [_P, _I64, _I32, _I32, _P, _P, _P]),
+    "moe_route_scored": (_I32, [C.POINTER(RouteDesc), _P, _P, _P, _P, _P]),
+    "moe_route_scored_backward": (_I32, [C.POINTER(RouteDesc), _P, _P, _P, _P, _P]),
     "moe_layout_m_cap": (_I64, [C.POINTER(LayoutDesc)]),
     "moe_layout_workspace_bytes": (_SZ, [C.POINTER(LayoutDesc)]),
     "moe_layout": (_I32, [C.POINTER(LayoutDesc), _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P,

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -96,6 +97,42 @@ int32_t moe_route(const float* logits_d, int64_t num_tokens, int32_t num_experts
   if (!logits_d || !topk_idx_d || !topk_w_d) return MOE_ERR_ARG;
   return status_of(moe::launch_route(logits_d, num_tokens, num_experts, top_k, topk_idx_d,
                                      topk_w_d, as_stream(stream)));
+}
+
+static int32_t route_desc_status(const moe_route_desc* d) {
+  if (!d || d->num_tokens < 0 || d->num_experts < 1 || d->num_experts > kMaxExperts)
+    return MOE_ERR_ARG;
+  if (d->score != MOE_SCORE_SOFTMAX && d->score != MOE_SCORE_SIGMOID) return MOE_ERR_ARG;
+  if (d->group_rank != MOE_GROUP_MAX && d->group_rank != MOE_GROUP_TOP2) return MOE_ERR_ARG;
+  if (d->num_groups < 1 || d->num_groups > 64 || d->num_experts % d->num_groups ||
+      d->top_groups < 1 || d->top_groups > d->num_groups)
+    return MOE_ERR_ARG;
+  if (d->top_k < 1 ||
+      d->top_k > std::min(kMaxTopK, d->top_groups * (d->num_experts / d->num_groups)))
+    return MOE_ERR_ARG;
+  if (d->renormalise != 0 && d->renormalise != 1) return MOE_ERR_ARG;
+  if (!std::isfinite(d->scale)) return MOE_ERR_ARG;
+  if (d->num_tokens > (int64_t(1) << 31) / d->top_k) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+
+int32_t moe_route_scored(const moe_route_desc* desc, const float* logits_d, const float* bias_d,
+                         int32_t* topk_idx_d, float* topk_w_d, void* stream) {
+  const int32_t st = route_desc_status(desc);
+  if (st != MOE_OK || desc->num_tokens == 0) return st;
+  if (!logits_d || !topk_idx_d || !topk_w_d) return MOE_ERR_ARG;
+  return status_of(moe::launch_route_scored(*desc, logits_d, bias_d, topk_idx_d, topk_w_d,
+                                            as_stream(stream)));
+}
+
+int32_t moe_route_scored_backward(const moe_route_desc* desc, const float* logits_d,
+                                  const int32_t* topk_idx_d, const float* grad_w_d,
+                                  float* grad_logits_d, void* stream) {
+  const int32_t st = route_desc_status(desc);
+  if (st != MOE_OK || desc->num_tokens == 0) return st;
+  if (!logits_d || !topk_idx_d || !grad_w_d || !grad_logits_d) return MOE_ERR_ARG;
+  return status_of(moe::launch_route_scored_backward(*desc, logits_d, topk_idx_d, grad_w_d,
+                                                     grad_logits_d, as_stream(stream)));
 }
 
 int64_t moe_layout_m_cap(const moe_layout_desc* desc) {

@@ -135,10 +135,18 @@ __device__ __forceinline__ void for_each_index(F&& f, std::integer_sequence<int,
 // ---------------------------------------------------------------------------
 // Host-side launchers, one per kernel family (defined in the .hip files).
 // They assume arguments were checked by the C ABI layer.
+struct moe_route_desc;
+
 namespace moe {
 
 hipError_t launch_route(const float* logits, int64_t T, int E, int k, int32_t* idx, float* w,
                         hipStream_t s);
+
+hipError_t launch_route_scored(const moe_route_desc& d, const float* logits, const float* bias,
+                               int32_t* idx, float* w, hipStream_t s);
+hipError_t launch_route_scored_backward(const moe_route_desc& d, const float* logits,
+                                        const int32_t* idx, const float* gw, float* out,
+                                        hipStream_t s);
 
 struct LayoutPlan {
   int64_t T;

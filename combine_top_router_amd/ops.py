@@ -12,7 +12,7 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import LayoutDesc, MoEError, check, lib
+from ._lib import LayoutDesc, MoEError, RouteDesc, check, lib
 
 
 def _stream(dev: torch.device):
@@ -54,6 +54,72 @@ def route(logits: torch.Tensor, top_k: int, topk_idx=None, topk_w=None):
     check("moe_route", lib().moe_route(_ptr(logits), T, E, top_k, _ptr(topk_idx), _ptr(topk_w),
                                        _stream(dev)))
     return topk_idx, topk_w
+
+
+# ---------------------------------------------------------------- scored route
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_RANKS = {"max": 0, "top2": 1}
+
+
+def _one_of(table: dict, key, name: str) -> int:
+    if key not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)} (got {key!r})")
+    return table[key]
+
+
+def _same_device(dev: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+
+
+def route_scored(logits: torch.Tensor, top_k: int, bias=None, score: str = "sigmoid",
+                 num_groups: int = 1, top_groups: int = 1, group_rank: str = "top2",
+                 renormalise: bool = True, scale: float = 1.0, topk_idx=None, topk_w=None):
+    """(topk_idx [T, k] int32, topk_w [T, k] float32) from logits [T, E] fp32:
+    the k experts with the largest score + bias among the ``top_groups`` groups
+    of the highest rank (a group's largest value, or the sum of its two
+    largest), weighted by their scores times ``scale``, renormalised over the k
+    if asked."""
+    _need(logits, "logits", torch.float32)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    topk_idx = _empty((T, top_k), torch.int32, dev) if topk_idx is None else topk_idx
+    topk_w = _empty((T, top_k), torch.float32, dev) if topk_w is None else topk_w
+    _need(topk_idx, "topk_idx", torch.int32, (T, top_k))
+    _need(topk_w, "topk_w", torch.float32, (T, top_k))
+    _same_device(dev, bias=bias, topk_idx=topk_idx, topk_w=topk_w)
+    desc = RouteDesc(T, E, top_k, _one_of(_SCORES, score, "score"), num_groups, top_groups,
+                     _one_of(_RANKS, group_rank, "group_rank"), int(bool(renormalise)), scale)
+    with torch.cuda.device(dev):
+        check("moe_route_scored", lib().moe_route_scored(
+            C.byref(desc), _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_w), _stream(dev)))
+    return topk_idx, topk_w
+
+
+def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: torch.Tensor,
+                          score: str = "sigmoid", renormalise: bool = True, scale: float = 1.0,
+                          out=None) -> torch.Tensor:
+    """grad_logits [T, E] fp32 from the gradient grad_w [T, k] of route_scored's
+    weights (same score, renormalise and scale), the choice held fixed."""
+    _need(logits, "logits", torch.float32)
+    T, E = logits.shape
+    dev = logits.device
+    _need(topk_idx, "topk_idx", torch.int32, (T, topk_idx.shape[-1]))
+    k = topk_idx.shape[1]
+    _need(grad_w, "grad_w", torch.float32, (T, k))
+    out = _empty((T, E), torch.float32, dev) if out is None else out
+    _need(out, "grad_logits", torch.float32, (T, E))
+    _same_device(dev, topk_idx=topk_idx, grad_w=grad_w, grad_logits=out)
+    desc = RouteDesc(T, E, k, _one_of(_SCORES, score, "score"), 1, 1, 0, int(bool(renormalise)),
+                     scale)
+    with torch.cuda.device(dev):
+        check("moe_route_scored_backward", lib().moe_route_scored_backward(
+            C.byref(desc), _ptr(logits), _ptr(topk_idx), _ptr(grad_w), _ptr(out), _stream(dev)))
+    return out
 
 
 # ---------------------------------------------------------------- layout

@@ -78,6 +78,67 @@ int32_t moe_route(const float* logits_d, int64_t num_tokens, int32_t num_experts
                   int32_t top_k, int32_t* topk_idx_d, float* topk_w_d, void* stream);
 
 /*
+ * moe_route_scored -- routing by scores, with a selection bias, groups of
+ * experts and a choice of normalisation. Per token:
+ *
+ *   s_e = sigmoid(l_e), or softmax(l)_e over all E experts
+ *   v_e = s_e + bias[e]          (bias NULL: v = s; the bias steers the choice, not the weights)
+ *   experts [g*E/G, (g+1)*E/G) form group g of G = num_groups; a group's rank is its largest
+ *   v (MOE_GROUP_MAX) or the sum of its two largest (MOE_GROUP_TOP2; a group of one expert:
+ *   its v); the top_groups groups of the highest rank stay
+ *   the k experts of those groups with the largest v, in descending order
+ *   w_j = scale * s_j, or with renormalise scale * s_j / (sum of s over the k selected)
+ *
+ * ties to the lower index. Scores, ranks and weights are formed in fp64, so the
+ * choice does not depend on how an fp32 exponential rounds; the weights are
+ * rounded once. A NaN logit counts as -inf, +inf as the largest finite fp32; an
+ * expert at -inf has score 0 and stays selectable. v = NaN (from the bias)
+ * counts as -inf. Renormalised weights whose sum is 0 are all 0.
+ *
+ *   logits_d    [T, E] float
+ *   bias_d      [E] float, or NULL
+ *   topk_idx_d  [T, k] int32 (out);  topk_w_d [T, k] float (out)
+ * Limits: T >= 0, 1 <= E <= 1024, 1 <= num_groups <= 64 dividing E,
+ * 1 <= top_groups <= num_groups, 1 <= k <= min(16, top_groups * E / num_groups),
+ * finite scale. T = 0 is a no-op.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+typedef struct moe_route_desc {
+  int64_t num_tokens;  /* T */
+  int32_t num_experts; /* E */
+  int32_t top_k;       /* k */
+  int32_t score;       /* MOE_SCORE_* */
+  int32_t num_groups;  /* 1: no groups */
+  int32_t top_groups;
+  int32_t group_rank;  /* MOE_GROUP_*; no effect when every group stays */
+  int32_t renormalise; /* 0 or 1 */
+  float scale;
+} moe_route_desc;
+
+int32_t moe_route_scored(const moe_route_desc* desc, const float* logits_d, const float* bias_d,
+                         int32_t* topk_idx_d, float* topk_w_d, void* stream);
+
+/*
+ * moe_route_scored_backward -- the gradient of moe_route_scored's weights
+ * with respect to the logits, the choice held fixed (the bias has none), from
+ * g = grad_w[t, :]. desc as in the forward; its groups are not used.
+ *
+ *   sigmoid:              dl_j = scale * g_j s_j (1 - s_j)
+ *   sigmoid, renormalise: dl_j = scale * (g_j - sum_i g_i s_i / S) / S * s_j (1 - s_j), S = sum_i s_i
+ *   softmax:              dl_e = scale * s_e (g_e - sum_i g_i s_i), every e; g_e = 0 unselected
+ *   softmax, renormalise: dl_j = scale * q_j (g_j - sum_i g_i q_i), q the renormalised weights / scale
+ *
+ * and 0 for the experts a formula does not name. A slot whose id is outside
+ * [0, E) is skipped; a repeated id takes the sum of its slots.
+ *   logits_d [T, E];  topk_idx_d, grad_w_d [T, k];  grad_logits_d [T, E] float (out)
+ */
+int32_t moe_route_scored_backward(const moe_route_desc* desc, const float* logits_d,
+                                  const int32_t* topk_idx_d, const float* grad_w_d,
+                                  float* grad_logits_d, void* stream);
+
+/*
  * Layout of one GPU's share when `ep_size` virtual ranks split the work:
  * source rank s owns tokens [s*T/ep, (s+1)*T/ep); destination rank d owns
  * experts [d*E/ep, (d+1)*E/ep); this GPU is destination `local_rank`
