@@ -11,7 +11,7 @@ from ._lib import LIB_PATH, MoEError, lib  # noqa: F401
 from .ops import (  # noqa: F401
     Layout, alloc_layout, combine, grouped_down, grouped_gate_up, grouped_gate_up_gather,
     grouped_swiglu, layout,
-    layout_desc, layout_m_cap, layout_workspace_bytes, pack_weights, permute, route,
+    layout_desc, layout_m_cap, layout_workspace_bytes, linear, linear_backward, pack_weights, permute, route,
     route_scored, route_scored_backward, validate_layout,
 )
 from .layer import MoELayer  # noqa: F401

@@ -34,6 +34,13 @@ class RouteDesc(C.Structure):
                 ("group_rank", C.c_int32), ("renormalise", C.c_int32), ("scale", C.c_float)]
 
 
+class LinearDesc(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("inner", C.c_int32), ("cols", C.c_int32),
+                ("dtype", C.c_int32), ("w_order", C.c_int32), ("act", C.c_int32),
+                ("y_f32", C.c_int32), ("ldx", C.c_int64), ("ldw", C.c_int64),
+                ("ldy", C.c_int64), ("ldr", C.c_int64), ("ldp", C.c_int64)]
+
+
 _P = C.c_void_p
 _I32, _I64, _SZ = C.c_int32, C.c_int64, C.c_size_t
 
@@ -66,6 +73,11 @@ SIGNATURES = {
     "moe_grouped_gate_up_backward": (_I32, [_P, _P, _P, _I32, _I64, _I32, _I32, _P, _P, _P, _P]),
     "moe_grouped_gate_up_wgrad": (_I32, [_P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _P, _P]),
     "moe_grouped_down_wgrad": (_I32, [_P, _P, _P, _P, _I32, _I64, _I32, _I32, _P, _P]),
+    "moe_linear_workspace_bytes": (_SZ, [C.POINTER(LinearDesc)]),
+    "moe_linear_backward_workspace_bytes": (_SZ, [C.POINTER(LinearDesc)]),
+    "moe_linear": (_I32, [C.POINTER(LinearDesc), _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_linear_backward": (_I32, [C.POINTER(LinearDesc), _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
+                                   _P]),
     "moe_combine": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _P]),
     "moe_combine_backward": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
     "moe_permute_backward": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _P, _P]),

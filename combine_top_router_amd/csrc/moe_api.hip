@@ -488,6 +488,75 @@ int32_t moe_combine_rows(const void* y_d, int32_t row_dtype, int64_t y_rows,
                                             num_tokens, hidden, top_k, out_d, as_stream(stream)));
 }
 
+static int32_t linear_desc_status(const moe_linear_desc* d) {
+  constexpr int32_t kDim = 1 << 20;
+  constexpr int64_t kStride = int64_t(1) << 21;
+  if (!d || d->rows < 0 || d->rows >= (int64_t(1) << 31) || d->inner < 8 || d->inner > kDim ||
+      d->cols < 1 || d->cols > kDim)
+    return MOE_ERR_ARG;
+  if (d->w_order != MOE_W_NK && d->w_order != MOE_W_KN) return MOE_ERR_ARG;
+  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU) return MOE_ERR_ARG;
+  if (d->y_f32 != 0 && d->y_f32 != 1) return MOE_ERR_ARG;
+  if (d->dtype != MOE_ROWS_BF16 && d->dtype != MOE_ROWS_F16) return MOE_ERR_UNSUPPORTED;
+  const bool nk = d->w_order == MOE_W_NK;
+  if (d->ldx < d->inner || d->ldw < (nk ? d->inner : d->cols) || d->ldy < d->cols)
+    return MOE_ERR_ARG;
+  if (d->ldx > kStride || d->ldw > kStride || d->ldy > kStride) return MOE_ERR_ARG;
+  if (d->inner % 8 || d->ldx % 8 || d->ldw % 8 || (!nk && d->cols % 8))
+    return MOE_ERR_UNSUPPORTED;
+  // a launch's workgroups (of at least 32 x 128 outputs) are counted in 32 bits
+  const int64_t big = std::max(d->inner, d->cols);
+  if ((d->rows / 128 + 1) * (big / 32 + 1) > (int64_t(1) << 31) / 512) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_linear_workspace_bytes(const moe_linear_desc* desc) {
+  return linear_desc_status(desc) == MOE_OK ? moe::linear_workspace_bytes(*desc) : 0;
+}
+
+size_t moe_linear_backward_workspace_bytes(const moe_linear_desc* desc) {
+  return linear_desc_status(desc) == MOE_OK ? moe::linear_backward_workspace_bytes(*desc) : 0;
+}
+
+static bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws && aligned16(ws) && have >= need);
+}
+
+int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d,
+                   const float* bias_d, const void* residual_d, void* y_d, void* pre_d,
+                   void* workspace_d, size_t workspace_bytes, void* stream) {
+  const int32_t st = linear_desc_status(desc);
+  if (st != MOE_OK || desc->rows == 0) return st;
+  if (!x_d || !w_d || !y_d || !aligned16(x_d) || !aligned16(w_d)) return MOE_ERR_ARG;
+  if ((residual_d && desc->ldr < desc->cols) || (pre_d && desc->ldp < desc->cols))
+    return MOE_ERR_ARG;
+  if (pre_d && (pre_d == y_d || pre_d == residual_d)) return MOE_ERR_ARG;
+  if (residual_d == y_d && (desc->y_f32 || desc->ldr != desc->ldy)) return MOE_ERR_ARG;
+  if (!workspace_ok(workspace_d, workspace_bytes, moe::linear_workspace_bytes(*desc)))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_linear(*desc, x_d, w_d, bias_d, residual_d, y_d, pre_d,
+                                      workspace_d, as_stream(stream)));
+}
+
+int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const void* x_d,
+                            const void* w_d, const void* pre_d, void* dx_d, void* dw_d,
+                            float* dbias_d, void* workspace_d, size_t workspace_bytes,
+                            void* stream) {
+  const int32_t st = linear_desc_status(desc);
+  if (st != MOE_OK || (!dx_d && !dw_d && !dbias_d)) return st;
+  if (desc->rows > 0) {
+    if (!dy_d) return MOE_ERR_ARG;
+    if (desc->act != MOE_ACT_NONE && (!pre_d || desc->ldp < desc->cols)) return MOE_ERR_ARG;
+    if (dx_d && (!w_d || !aligned16(w_d))) return MOE_ERR_ARG;
+    if (dw_d && (!x_d || !aligned16(x_d))) return MOE_ERR_ARG;
+  }
+  if (!aligned16(dx_d) || !aligned16(dw_d)) return MOE_ERR_ARG;
+  if (!workspace_ok(workspace_d, workspace_bytes, moe::linear_backward_workspace_bytes(*desc)))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_linear_backward(*desc, dy_d, x_d, w_d, pre_d, dx_d, dw_d, dbias_d,
+                                               workspace_d, as_stream(stream)));
+}
+
 int32_t moe_validate_layout(const moe_layout_desc* desc, const int32_t* topk_idx_d,
                             const int32_t* offsets_d, const int32_t* dst_row_d,
                             const int32_t* src_row_d, int64_t m_cap, void* stream, char* detail,

@@ -136,6 +136,7 @@ __device__ __forceinline__ void for_each_index(F&& f, std::integer_sequence<int,
 // Host-side launchers, one per kernel family (defined in the .hip files).
 // They assume arguments were checked by the C ABI layer.
 struct moe_route_desc;
+struct moe_linear_desc;
 
 namespace moe {
 
@@ -182,6 +183,14 @@ hipError_t launch_combine_backward(const void* grad_out, const void* y, int64_t 
 hipError_t launch_route_backward(const int32_t* topk_idx, const float* topk_w,
                                  const float* grad_w, int64_t T, int E, int k,
                                  float* grad_logits, hipStream_t s);
+size_t linear_workspace_bytes(const moe_linear_desc& d);
+size_t linear_backward_workspace_bytes(const moe_linear_desc& d);
+hipError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w,
+                         const float* bias, const void* residual, void* y, void* pre, void* ws,
+                         hipStream_t s);
+hipError_t launch_linear_backward(const moe_linear_desc& d, const void* dy, const void* x,
+                                  const void* w, const void* pre, void* dx, void* dw,
+                                  float* dbias, void* ws, hipStream_t s);
 // Packed expert-weight layout (written by launch_pack, read by the forward
 // grouped GEMMs): for each matrix, its N output rows form blocks of
 // R = packed_row_block(N) rows, and each block is stored as K / kPackedSlice

@@ -12,7 +12,7 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import LayoutDesc, MoEError, RouteDesc, check, lib
+from ._lib import LayoutDesc, LinearDesc, MoEError, RouteDesc, check, lib
 
 
 def _stream(dev: torch.device):
@@ -328,6 +328,146 @@ def grouped_swiglu(x_perm, offsets, counts, w1t, w3t, w2t, h=None, out=None):
         _ptr(x_perm), _ptr(offsets), _ptr(counts), e_loc, m_cap, H, I, _ptr(w1t), _ptr(w3t),
         _ptr(w2t), _ptr(h), _ptr(out), _stream(x_perm.device)))
     return out
+
+
+# ---------------------------------------------------------------- linear
+
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+_LINEAR_ROWS = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Checks a [rows, cols] tensor whose rows may lie apart; returns their stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on the GPU (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    rows, cols = t.shape
+    if rows <= 1:  # a single row's stride is never used
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return (cols + 7) // 8 * 8
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise ValueError(f"{name} must have contiguous rows (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _linear_desc(x, w, act, y_f32, ldy):
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    if x.dtype not in _LINEAR_ROWS:
+        raise TypeError(f"x must be bf16 or fp16 (got {x.dtype})")
+    M, K = x.shape
+    N = w.shape[0]
+    ldx = _need_rows(x, "x", x.dtype, (M, K))
+    kn = w.stride(1) != 1 and w.stride(0) == 1  # a transposed [inner, cols] matrix
+    ldw = _need_rows(w.t(), "w.t()", x.dtype, (K, N)) if kn else _need_rows(w, "w", x.dtype, (N, K))
+    return LinearDesc(M, K, N, _LINEAR_ROWS[x.dtype], int(kn), _one_of(_ACTS, act, "act"),
+                      int(y_f32), ldx, ldw, ldy, 0, 0)
+
+
+def _linear_workspace(need: int, given, dev):
+    if given is None:
+        return _empty((need,), torch.uint8, dev) if need else None
+    _need(given, "workspace", torch.uint8)
+    if given.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes (got {given.numel()})")
+    return given
+
+
+def linear_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
+    """Bytes of workspace ``linear`` needs on these operands (often 0)."""
+    return int(lib().moe_linear_workspace_bytes(C.byref(_linear_desc(x, w, "none", 0, w.shape[0]))))
+
+
+def linear_backward_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
+    """Bytes of workspace ``linear_backward`` needs on these operands."""
+    return int(lib().moe_linear_backward_workspace_bytes(
+        C.byref(_linear_desc(x, w, "none", 0, w.shape[0]))))
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none", residual=None,
+           out_dtype=None, out=None, pre=None, workspace=None) -> torch.Tensor:
+    """act(x w^T + bias) + residual: x [M, K], w [N, K] bf16 or fp16 (w contiguous, or
+    the transpose of a contiguous [K, N] matrix), bias [N] fp32, residual [M, N]
+    as x; the result as x or fp32. ``pre``, if given, receives x w^T + bias for
+    linear_backward. ``out`` may be ``residual``. fp32 sums, one rounding."""
+    dev = x.device
+    M, N = x.shape[0], w.shape[0]
+    if out is None:
+        dt = x.dtype if out_dtype is None else out_dtype
+        out = _empty((M, N), dt, dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype} (got {out.dtype})")
+    if out.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"out must be {x.dtype} or fp32 (got {out.dtype})")
+    desc = _linear_desc(x, w, act, out.dtype == torch.float32,
+                        _need_rows(out, "out", out.dtype, (M, N)))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (N,))
+    if residual is not None:
+        desc.ldr = _need_rows(residual, "residual", x.dtype, (M, N))
+    if pre is not None:
+        desc.ldp = _need_rows(pre, "pre", x.dtype, (M, N))
+    _same_device(dev, w=w, bias=bias, residual=residual, out=out, pre=pre, workspace=workspace)
+    ws = _linear_workspace(int(lib().moe_linear_workspace_bytes(C.byref(desc))), workspace, dev)
+    with torch.cuda.device(dev):
+        check("moe_linear", lib().moe_linear(
+            C.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), _ptr(pre),
+            _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    return out
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "none",
+                    pre=None, want_dx: bool = True, want_dw: bool = True,
+                    want_dbias: bool = False, dx=None, dw=None, dbias=None, workspace=None):
+    """(dx [M, K], dw [N, K], dbias [N] fp32) from dy [M, N] (as x, or fp32), None
+    for those not wanted. ``pre`` is linear's pre-activation (for act other than
+    "none"); dw lies in memory as w does. The residual's gradient is dy."""
+    dev = x.device
+    M, K = x.shape
+    N = w.shape[0]
+    if dy.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"dy must be {x.dtype} or fp32 (got {dy.dtype})")
+    desc = _linear_desc(x, w, act, dy.dtype == torch.float32,
+                        _need_rows(dy, "dy", dy.dtype, (M, N)))
+    if act != "none":
+        if pre is None:
+            raise ValueError(f"act {act!r} needs the pre-activation")
+        desc.ldp = _need_rows(pre, "pre", x.dtype, (M, N))
+    else:
+        pre = None
+    if want_dx:
+        dx = _empty((M, K), x.dtype, dev) if dx is None else dx
+        _need(dx, "dx", x.dtype, (M, K))
+    else:
+        dx = None
+    if want_dw:
+        if desc.w_order:
+            dw = _empty((K, N), x.dtype, dev).t() if dw is None else dw
+            _need(dw.t(), "dw.t()", x.dtype, (K, N))
+        else:
+            dw = _empty((N, K), x.dtype, dev) if dw is None else dw
+            _need(dw, "dw", x.dtype, (N, K))
+    else:
+        dw = None
+    if want_dbias:
+        dbias = _empty((N,), torch.float32, dev) if dbias is None else dbias
+        _need(dbias, "dbias", torch.float32, (N,))
+    else:
+        dbias = None
+    _same_device(dev, dy=dy, w=w, pre=pre, dx=dx, dw=dw, dbias=dbias, workspace=workspace)
+    ws = _linear_workspace(int(lib().moe_linear_backward_workspace_bytes(C.byref(desc))),
+                           workspace, dev)
+    with torch.cuda.device(dev):
+        check("moe_linear_backward", lib().moe_linear_backward(
+            C.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(pre), _ptr(dx), _ptr(dw),
+            _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    return dx, dw, dbias
 
 
 # ---------------------------------------------------------------- combine

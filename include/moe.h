@@ -50,6 +50,9 @@ typedef enum moe_status {
                                library's static array holds */
 } moe_status;
 
+/* Types of row buffers, for the calls that take more than bf16. */
+enum { MOE_ROWS_BF16 = 0, MOE_ROWS_F16 = 1, MOE_ROWS_F32 = 2 };
+
 /* Static name of a status code ("MOE_OK", ...); never NULL. */
 const char* moe_status_string(int32_t status);
 
@@ -449,6 +452,75 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
                                void* stream);
 
 /*
+ * moe_linear -- dense matrix product with bias, activation and residual.
+ *
+ *   z = x w^T + bias          fp32 sums of the 16-bit products, bias added in fp32
+ *   y = act(z) + residual     fp32, rounded once to y's type
+ *   pre = z, rounded to the rows' type (kept for moe_linear_backward; NULL: not stored)
+ *
+ * act: none, relu, silu z / (1 + e^-z), or gelu z Phi(z) (Phi the normal
+ * distribution function). The router projection (fp32 logits from 16-bit
+ * rows), a shared expert's products and dense layers.
+ *   x_d         [rows, inner], row stride ldx;  w_d: MOE_W_NK [cols, inner] or MOE_W_KN
+ *               [inner, cols], row stride ldw; both of `dtype`, 16-byte aligned
+ *   bias_d      [cols] float, or NULL
+ *   residual_d  [rows, cols] of `dtype`, row stride ldr, or NULL
+ *   y_d         [rows, cols] of `dtype` or (y_f32) float, row stride ldy (out)
+ *   pre_d       [rows, cols] of `dtype`, row stride ldp, or NULL (out)
+ * y may be the residual itself (same address, stride and type); other buffers
+ * must not overlap. Strides are in elements; ldr and ldp are read only where their buffer is given.
+ * A masked row's values reach that row of y alone.
+ * Limits: 0 <= rows < 2^31, 8 <= inner, 1 <= cols, both <= 2^20; dtype MOE_ROWS_BF16 or
+ * MOE_ROWS_F16; inner, ldx and ldw multiples of 8; MOE_W_KN: cols a multiple of 8 too
+ * (else MOE_ERR_UNSUPPORTED); strides at least the row length; ldx, ldw and ldy at most 2^21.
+ *   workspace_d >= moe_linear_workspace_bytes(desc) bytes, 16-byte aligned (NULL if that
+ *   is 0); contents on entry do not matter. Calls that may overlap need workspaces of their own.
+ */
+enum { MOE_W_NK = 0, MOE_W_KN = 1 };
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
+
+typedef struct moe_linear_desc {
+  int64_t rows;    /* M */
+  int32_t inner;   /* K */
+  int32_t cols;    /* N */
+  int32_t dtype;   /* MOE_ROWS_BF16 or MOE_ROWS_F16 */
+  int32_t w_order; /* MOE_W_* */
+  int32_t act;     /* MOE_ACT_* */
+  int32_t y_f32;   /* 0: y (backward: dy) of dtype, 1: float */
+  int64_t ldx, ldw, ldy, ldr, ldp;
+} moe_linear_desc;
+
+/* Bytes of workspace of the two calls (0 for an invalid descriptor). */
+size_t moe_linear_workspace_bytes(const moe_linear_desc* desc);
+size_t moe_linear_backward_workspace_bytes(const moe_linear_desc* desc);
+
+int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d,
+                   const float* bias_d, const void* residual_d, void* y_d, void* pre_d,
+                   void* workspace_d, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_linear_backward -- gradients of moe_linear from dy [rows, cols] (of
+ * dtype, or float with y_f32; row stride ldy) and the pre-activation:
+ *
+ *   dz = dy act'(pre)   fp32, then rounded to dtype for the two products (the
+ *                       matrix cores read 16-bit values; this is the size of
+ *                       the rounding the outputs have themselves)
+ *   dx = dz w           [rows, inner] of dtype, dense
+ *   dw = dz^T x         in w's order, of dtype, dense
+ *   dbias = column sums of the unrounded dz, [cols] float
+ *
+ * fp32 sums, one rounding per output; the residual's gradient is dy. dx_d,
+ * dw_d and dbias_d may each be NULL to skip it. pre_d is needed unless act is none, w_d
+ * for dx, x_d for dw. With fp16 rows, dz below fp16's range is lost: scale the loss.
+ * rows = 0 sets dw and dbias to zero. dx_d and dw_d 16-byte aligned; limits and
+ * workspace as moe_linear, with moe_linear_backward_workspace_bytes.
+ */
+int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const void* x_d,
+                            const void* w_d, const void* pre_d, void* dx_d, void* dw_d,
+                            float* dbias_d, void* workspace_d, size_t workspace_bytes,
+                            void* stream);
+
+/*
  * moe_combine -- fused weighted-sum restore.
  *
  * The fused restore of DeepSpeed PR #8847 ("AutoEP: support
@@ -541,8 +613,6 @@ int32_t moe_route_backward(const int32_t* topk_idx_d, const float* topk_w_d,
  * the row dtype; MOE_ROWS_BF16 with weights and no shared rows is moe_combine.
  * Limits as moe_combine.
  */
-enum { MOE_ROWS_BF16 = 0, MOE_ROWS_F16 = 1, MOE_ROWS_F32 = 2 };
-
 int32_t moe_combine_rows(const void* y_d, int32_t row_dtype, int64_t y_rows,
                          const int32_t* dst_row_d, const float* topk_w_d, const void* shared_d,
                          int64_t num_tokens, int32_t hidden, int32_t top_k, void* out_d,

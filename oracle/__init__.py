@@ -5,6 +5,7 @@ method does floating point) of what the HIP library computes:
 
   route    -> ``oracle.route``     token-choice top-k routing
   route_scored -> ``oracle.route_scored``  softmax / sigmoid scores, bias, groups; its gradient
+  linear   -> ``oracle.linear``    dense product with bias, activation, residual; its gradients
   layout   -> ``oracle.layout``    histogram, split plan, padded offsets, stable permutation
   permute  -> ``oracle.permute``   expert-major row gather
   experts  -> ``oracle.experts``   per-expert SwiGLU MLP
@@ -21,4 +22,4 @@ Pinned by ``tests/test_oracle_*.py`` against a hand-computed worked example
 invariants the pages state. Parity unpinned: nothing (every function has at
 least one pin that does not re-run its own formula).
 """
-from . import backward, bf16, checks, combine, experts, layer, layout, permute, route, route_scored  # noqa: F401
+from . import backward, bf16, checks, combine, experts, layer, layout, linear, permute, route, route_scored  # noqa: F401

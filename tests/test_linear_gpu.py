@@ -1,0 +1,305 @@
+"""GPU parity of the dense linear layer and its gradients against the float64
+oracle. Bounds: u is half a step of the 16-bit type; the products are exact in
+fp32, a sum of K of them is off by at most K steps of 2^-23 of the sum of their
+magnitudes; activations change an error by at most 1.13 (gelu's steepest slope)
+and are evaluated in fp32 within 2^-20 of |z| (slopes: of 1)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import linear as olinear
+
+pytestmark = pytest.mark.gpu
+moe = pytest.importorskip("combine_top_router_amd")
+ops = moe.ops
+
+BF, FP = torch.bfloat16, torch.float16
+HALF_STEP = {BF: 2.0 ** -8, FP: 2.0 ** -11, torch.float32: 2.0 ** -24}
+TINY = {BF: 2.0 ** -133, FP: 2.0 ** -24, torch.float32: 2.0 ** -149}
+
+# rows, inner, cols: single rows, odd and ragged sizes, every tile shape, split and not
+SHAPES = [
+    (1, 8, 1), (1, 64, 8), (3, 72, 5), (17, 7168, 256), (33, 136, 130), (64, 4096, 1000),
+    (129, 264, 257), (300, 520, 520), (1000, 1024, 60), (513, 2056, 776), (2048, 512, 2048),
+    (700, 64, 16), (5, 16, 4096), (4100, 200, 8), (256, 2048, 40), (1023, 4104, 300),
+]
+ACTS = ["none", "relu", "silu", "gelu"]
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _close(got, want, tol, what):
+    g = f64(got)
+    bad = ~(np.abs(g - want) <= tol)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:4], g[bad][:4], want[bad][:4])
+
+
+def _matrix(gen, rows, cols, dtype, pad=0, std=1.0):
+    """Random [rows, cols]; with pad, a view of wider rows whose rest is NaN."""
+    v = (torch.randn((rows, cols), generator=gen, device="cuda") * std).to(dtype)
+    if not pad:
+        return v
+    wide = torch.full((rows + 1, cols + pad), float("nan"), dtype=dtype, device="cuda")
+    wide[:rows, :cols] = v
+    return wide[:rows, :cols]
+
+
+def _forward(gen, M, K, N, dtype, order, act, bias, res, keep, f32, pad=0, **kw):
+    x = _matrix(gen, M, K, dtype, pad)
+    w = _matrix(gen, N, K, dtype, pad, K ** -0.5) if order == "nk" else \
+        _matrix(gen, K, N, dtype, pad, K ** -0.5).t()
+    b = torch.randn((N,), generator=gen, device="cuda") if bias else None
+    r = _matrix(gen, M, N, dtype, pad and pad + 1) if res else None
+    pre = torch.empty((M, N), dtype=dtype, device="cuda") if keep else None
+    y = ops.linear(x, w, b, act, r, torch.float32 if f32 else None, pre=pre, **kw)
+    torch.cuda.synchronize()
+    xs, ws = f64(x), f64(w)
+    want, z = olinear.linear(xs, ws, None if b is None else f64(b), act, None if r is None else f64(r))
+    mag = np.abs(xs) @ np.abs(ws).T
+    ez = (K + 160) * 2.0 ** -23 * mag + 2.0 ** -23 * np.abs(z)  # up to 128 parts, and the bias
+    t = torch.float32 if f32 else dtype
+    ey = 1.13 * ez + 2.0 ** -20 * np.abs(z) + (2.0 ** -23 * (np.abs(want) + np.abs(z)))
+    _close(y, want, ey + HALF_STEP[t] * (np.abs(want) + ey) + TINY[t], "y")
+    if keep:
+        _close(pre, z, ez + HALF_STEP[dtype] * (np.abs(z) + ez) + TINY[dtype], "pre")
+    return x, w, b, r, y
+
+
+def _backward(gen, M, K, N, dtype, order, act, f32, pad=0, bias=True, **kw):
+    x = _matrix(gen, M, K, dtype, pad)
+    w = _matrix(gen, N, K, dtype, pad, K ** -0.5) if order == "nk" else \
+        _matrix(gen, K, N, dtype, pad, K ** -0.5).t()
+    pre = _matrix(gen, M, N, dtype, pad and pad + 3) if act != "none" else None
+    dy = _matrix(gen, M, N, torch.float32 if f32 else dtype, pad)
+    dx, dw, db = ops.linear_backward(dy, x, w, act, pre, want_dbias=bias, **kw)
+    torch.cuda.synchronize()
+    assert dw.stride() == ((K, 1) if order == "nk" else (1, N)) or 1 in (K, N)
+    xs, ws, dys = f64(x), f64(w), f64(dy)
+    wx, ww, wb, dz = olinear.linear_backward(dys, xs, ws, act, None if pre is None else f64(pre))
+    u = HALF_STEP[dtype]
+    # dz as the matrix cores read it
+    slope = 0.0 if act == "none" else 2.0 ** -20 * np.abs(dys)
+    edz = slope + u * (np.abs(dz) + slope) + TINY[dtype]
+    for got, want, other, n, what in ((dx, wx, np.abs(ws), N, "dx"),
+                                      (dw.t(), ww.T, np.abs(xs), M, "dw")):
+        if what == "dx":
+            mag, e = (np.abs(dz) + edz) @ other, edz @ other
+        else:
+            mag, e = other.T @ (np.abs(dz) + edz), other.T @ edz
+        e = e + (n + 160) * 2.0 ** -23 * mag
+        _close(got, want, e + u * (np.abs(want) + e) + TINY[dtype], what)
+    if bias:
+        eb = (slope + (M / 8 + 16) * 2.0 ** -24 * np.abs(dz)).sum(axis=0)
+        _close(db, wb, eb + 2.0 ** -24 * np.abs(wb) + 2.0 ** -149, "dbias")
+    else:
+        assert db is None
+    return dx, dw, db
+
+
+def _orders(N):
+    return ["nk", "kn"] if N % 8 == 0 else ["nk"]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_forward(shape, dtype):
+    M, K, N = shape
+    gen = torch.Generator("cuda").manual_seed(M + K + N)
+    for i, order in enumerate(_orders(N)):
+        for j, act in enumerate(ACTS):
+            print("CASE linear", shape, dtype, order, act, flush=True)
+            f32 = (i + j) % 2 == 1
+            _forward(gen, M, K, N, dtype, order, act, bias=j % 2 == 0, res=j >= 2,
+                     keep=(i + j) % 3 == 0, f32=f32)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_backward(shape, dtype):
+    M, K, N = shape
+    gen = torch.Generator("cuda").manual_seed(M * 3 + K + N)
+    for i, order in enumerate(_orders(N)):
+        for j, act in enumerate(ACTS):
+            print("CASE linear backward", shape, dtype, order, act, flush=True)
+            _backward(gen, M, K, N, dtype, order, act, f32=(i + j) % 2 == 1, bias=j < 3)
+
+
+@pytest.mark.parametrize("pad", [8, 24])
+@pytest.mark.parametrize("shape", [(37, 72, 40), (300, 200, 264), (40, 4096, 128), (600, 64, 16)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_rows_lying_apart_with_nan_between(shape, pad):
+    M, K, N = shape
+    gen = torch.Generator("cuda").manual_seed(pad)
+    for order in ("nk", "kn"):
+        print("CASE strides", shape, pad, order, flush=True)
+        _forward(gen, M, K, N, BF, order, "silu", True, True, True, False, pad)
+        _backward(gen, M, K, N, BF, order, "gelu", False, pad)
+        _backward(gen, M, K, N, FP, order, "none", False, pad)
+
+
+def test_output_views_leave_their_surroundings_alone():
+    gen = torch.Generator("cuda").manual_seed(9)
+    x, w = _matrix(gen, 45, 64, BF), _matrix(gen, 33, 64, BF)
+    plain = ops.linear(x, w)
+    for cols in (40, 41):  # aligned rows and odd ones
+        wide = torch.full((47, cols), 7.0, dtype=BF, device="cuda")
+        pre = torch.full((47, cols), 7.0, dtype=BF, device="cuda")
+        ops.linear(x, w, out=wide[1:46, :33], pre=pre[1:46, :33])
+        torch.cuda.synchronize()
+        for t in (wide, pre):
+            assert torch.equal(t[1:46, :33], plain)
+            t[1:46, :33] = 7.0
+            assert (t == 7.0).all()
+
+
+def test_residual_may_be_the_output():
+    gen = torch.Generator("cuda").manual_seed(10)
+    for M, K, N in ((70, 256, 96), (8, 8192, 64)):  # whole and split
+        x, w, r = _matrix(gen, M, K, BF), _matrix(gen, N, K, BF, 0, K ** -0.5), _matrix(gen, M, N, BF)
+        want = ops.linear(x, w, residual=r)
+        ops.linear(x, w, residual=r, out=r)
+        torch.cuda.synchronize()
+        assert torch.equal(r, want)
+
+
+def test_a_bad_row_or_column_stays_by_itself():
+    gen = torch.Generator("cuda").manual_seed(11)
+    for M, K, N in ((50, 72, 40), (300, 264, 300), (20, 4096, 64)):
+        x, w = _matrix(gen, M, K, BF), _matrix(gen, N, K, BF, 0, K ** -0.5)
+        want = ops.linear(x, w)
+        x2, w2 = x.clone(), w.clone()
+        x2[3], x2[-1, 0] = float("nan"), float("inf")
+        w2[5] = float("nan")
+        got = ops.linear(x2, w2)
+        torch.cuda.synchronize()
+        assert got[3].isnan().all() and got[:, 5].isnan().all()
+        keep = torch.ones_like(got, dtype=torch.bool)
+        keep[3], keep[-1], keep[:, 5] = False, False, False
+        assert torch.equal(got[keep], want[keep])
+        dy = _matrix(gen, M, N, BF)
+        dx, dw, _ = ops.linear_backward(dy, x, w)
+        dy[3] = float("nan")
+        dx2, _, _ = ops.linear_backward(dy, x, w, want_dw=False)
+        torch.cuda.synchronize()
+        assert dx2[3].isnan().all()
+        dx2[3] = dx[3]
+        assert torch.equal(dx2, dx)
+
+
+def test_same_result_twice_and_from_a_dirty_workspace():
+    gen = torch.Generator("cuda").manual_seed(12)
+    x, w, dy = _matrix(gen, 24, 6144, BF), _matrix(gen, 200, 6144, BF), _matrix(gen, 24, 200, BF)
+    y = ops.linear(x, w)
+    ws = torch.full((ops.linear_workspace_bytes(x, w),), 255, dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0 and torch.equal(ops.linear(x, w, workspace=ws), y)
+    a = ops.linear_backward(dy, x, w, want_dbias=True)
+    ws = torch.full((ops.linear_backward_workspace_bytes(x, w),), 255, dtype=torch.uint8,
+                    device="cuda")
+    b = ops.linear_backward(dy, x, w, want_dbias=True, workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_rows_past_32_bit_offsets():
+    M, K, N = 300_000, 8192, 24  # 4.9 GB of rows
+    gen = torch.Generator("cuda").manual_seed(13)
+    w = _matrix(gen, N, K, BF, 0, K ** -0.5)
+    x = torch.zeros((M, K), dtype=BF, device="cuda")
+    rows = [0, 1, 131071, 131072, 262143, 262144, 299_999]
+    for r in rows:
+        x[r] = torch.randn((K,), generator=gen, device="cuda").to(BF)
+    y = ops.linear(x, w, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want, _ = olinear.linear(f64(x[rows]), f64(w))
+    mag = np.abs(f64(x[rows])) @ np.abs(f64(w)).T
+    _close(y[rows], want, (K + 160) * 2.0 ** -23 * mag, "y")
+    y[rows] = 0
+    assert not y.any()
+    dy = torch.zeros((M, N), dtype=BF, device="cuda")
+    dy[rows] = torch.randn((len(rows), N), generator=gen, device="cuda").to(BF)
+    dx, dw, _ = ops.linear_backward(dy, x, w)
+    torch.cuda.synchronize()
+    wx, ww, _, dz = olinear.linear_backward(f64(dy[rows]), f64(x[rows]), f64(w))
+    ex = (N + 160) * 2.0 ** -23 * (np.abs(dz) @ np.abs(f64(w)))
+    _close(dx[rows], wx, ex + 2.0 ** -8 * (np.abs(wx) + ex), "dx")
+    ew = 200 * 2.0 ** -23 * (np.abs(dz).T @ np.abs(f64(x[rows])))
+    _close(dw, ww, ew + 2.0 ** -8 * (np.abs(ww) + ew), "dw")
+    dx[rows] = 0
+    assert not dx.any()
+
+
+def test_no_rows():
+    x, w = torch.empty((0, 64), dtype=BF, device="cuda"), torch.ones((24, 64), dtype=BF, device="cuda")
+    assert ops.linear(x, w).shape == (0, 24)
+    for ww in (w, torch.ones((64, 24), dtype=BF, device="cuda").t()):
+        dx, dw, db = ops.linear_backward(torch.empty((0, 24), dtype=BF, device="cuda"), x, ww,
+                                         want_dbias=True)
+        torch.cuda.synchronize()
+        assert dx.shape == (0, 64) and dw.shape == (24, 64) and not dw.any() and not db.any()
+
+
+def test_refusals():
+    x, w = torch.zeros((4, 64), dtype=BF, device="cuda"), torch.zeros((8, 64), dtype=BF, device="cuda")
+    with pytest.raises(TypeError):
+        ops.linear(x.float(), w)
+    with pytest.raises(TypeError):
+        ops.linear(x, w.half())
+    with pytest.raises(TypeError):
+        ops.linear(x, w, out_dtype=FP)
+    with pytest.raises(ValueError):
+        ops.linear(x, w, act="tanh")
+    with pytest.raises(ValueError):
+        ops.linear(x, w[:, :32])
+    with pytest.raises(ValueError):
+        ops.linear(x[:, ::2], w[:, ::2])
+    with pytest.raises(ValueError):
+        ops.linear(x, w, residual=torch.zeros((4, 9), dtype=BF, device="cuda"))
+    with pytest.raises(TypeError):
+        ops.linear(x, w, bias=torch.zeros((8,), dtype=BF, device="cuda"))
+    with pytest.raises(ValueError):
+        ops.linear(x[:1].expand(4, 64), w)
+    with pytest.raises(ValueError):
+        ops.linear(x.cpu(), w)
+    with pytest.raises(moe.MoEError):
+        ops.linear(x[:, :60].contiguous(), w[:, :60].contiguous())  # inner % 8
+    with pytest.raises(ValueError):
+        ops.linear_backward(torch.zeros((4, 8), dtype=BF, device="cuda"), x, w, act="silu")
+    with pytest.raises(TypeError):
+        ops.linear(x, w, workspace=torch.zeros((64,), device="cuda"))
+    long = torch.zeros((4, 8192), dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        ops.linear(long, long, workspace=torch.zeros((16,), dtype=torch.uint8, device="cuda"))
+
+
+def test_two_graphs_replay_between_eager_calls():
+    gen = torch.Generator("cuda").manual_seed(14)
+    sets = []
+    for M, K, N in ((16, 4096, 64), (300, 256, 512)):
+        x, w, dy = _matrix(gen, M, K, BF), _matrix(gen, N, K, BF, 0, K ** -0.5), _matrix(gen, M, N, BF)
+        pre = torch.empty((M, N), dtype=BF, device="cuda")
+
+        def step(x=x, w=w, dy=dy, pre=pre):
+            y = ops.linear(x, w, act="silu", pre=pre)
+            return (y,) + ops.linear_backward(dy, x, w, "silu", pre, want_dbias=True)
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        sets.append((graph, out, step, x))
+    for rep in range(3):
+        for graph, out, step, x in sets:
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda"))
+            want = [t.clone() for t in step()]
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
