@@ -9,9 +9,9 @@ with ``python -m combine_top_router_amd.build``.
 """
 from ._lib import LIB_PATH, MoEError, lib  # noqa: F401
 from .ops import (  # noqa: F401
-    Layout, alloc_layout, combine, grouped_down, grouped_gate_up, grouped_gate_up_gather,
-    grouped_swiglu, layout,
-    layout_desc, layout_m_cap, layout_workspace_bytes, linear, linear_backward, pack_weights, permute, route,
+    Layout, alloc_layout, clip_grad_norm, clip_grads, combine, grad_sumsq, grouped_down,
+    grouped_gate_up, grouped_gate_up_gather, grouped_swiglu, layout, layout_desc, layout_m_cap,
+    layout_workspace_bytes, linear, linear_backward, pack_weights, permute, route,
     route_scored, route_scored_backward, validate_layout,
 )
 from .layer import MoELayer  # noqa: F401

@@ -82,6 +82,9 @@ SIGNATURES = {
     "moe_combine_backward": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
     "moe_permute_backward": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _P, _P]),
     "moe_route_backward": (_I32, [_P, _P, _P, _I64, _I32, _I32, _P, _P]),
+    "moe_grad_sumsq_workspace_bytes": (_SZ, [_P, _I32]),
+    "moe_grad_sumsq": (_I32, [_P, _I32, _P, _P, _SZ, _P]),
+    "moe_grad_clip": (_I32, [_P, _I32, _P, C.c_float, _P, _P]),
     "moe_validate_layout": (_I32, [C.POINTER(LayoutDesc), _P, _P, _P, _P, _I64, _P, C.c_char_p,
                                    _SZ]),
 }

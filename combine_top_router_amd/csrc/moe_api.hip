@@ -557,6 +557,55 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
                                                workspace_d, as_stream(stream)));
 }
 
+static int32_t tensors_status(const moe_tensor_ref* t, int32_t n) {
+  if (n < 0 || n > 65536 || (n > 0 && !t)) return MOE_ERR_ARG;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].dtype != MOE_ROWS_BF16 && t[i].dtype != MOE_ROWS_F16 && t[i].dtype != MOE_ROWS_F32)
+      return MOE_ERR_UNSUPPORTED;
+    if (t[i].numel < 0 || t[i].numel >= (int64_t(1) << 44) || t[i].reserved) return MOE_ERR_ARG;
+    if (t[i].numel == 0) continue;
+    const uintptr_t mask = t[i].dtype == MOE_ROWS_F32 ? 3 : 1;
+    if (!t[i].data || (reinterpret_cast<uintptr_t>(t[i].data) & mask) ||
+        (reinterpret_cast<uintptr_t>(t[i].out) & mask))
+      return MOE_ERR_ARG;
+  }
+  return MOE_OK;
+}
+
+size_t moe_grad_sumsq_workspace_bytes(const moe_tensor_ref* tensors, int32_t num_tensors) {
+  return tensors_status(tensors, num_tensors) == MOE_OK
+             ? moe::grad_sumsq_workspace_bytes(tensors, num_tensors)
+             : 0;
+}
+
+int32_t moe_grad_sumsq(const moe_tensor_ref* tensors, int32_t num_tensors, double* sumsq_d,
+                       void* workspace_d, size_t workspace_bytes, void* stream) {
+  const int32_t st = tensors_status(tensors, num_tensors);
+  if (st != MOE_OK) return st;
+  const size_t need = moe::grad_sumsq_workspace_bytes(tensors, num_tensors);
+  if (!sumsq_d || (reinterpret_cast<uintptr_t>(sumsq_d) & 7)) return MOE_ERR_ARG;
+  if (need && (!workspace_d || (reinterpret_cast<uintptr_t>(workspace_d) & 7) ||
+               workspace_bytes < need))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_grad_sumsq(tensors, num_tensors, sumsq_d, workspace_d,
+                                          as_stream(stream)));
+}
+
+int32_t moe_grad_clip(const moe_tensor_ref* tensors, int32_t num_tensors, const double* sumsq_d,
+                      float max_norm, float* norm_d, void* stream) {
+  const int32_t st = tensors_status(tensors, num_tensors);
+  if (st != MOE_OK) return st;
+  if (!sumsq_d || (reinterpret_cast<uintptr_t>(sumsq_d) & 7) || !(max_norm >= 0.f))
+    return MOE_ERR_ARG;
+  try {
+    if (moe::grad_clip_overlaps(tensors, num_tensors)) return MOE_ERR_ARG;
+  } catch (...) {  // no host memory for the check
+    return MOE_ERR_HIP;
+  }
+  return status_of(moe::launch_grad_clip(tensors, num_tensors, sumsq_d, max_norm, norm_d,
+                                         as_stream(stream)));
+}
+
 int32_t moe_validate_layout(const moe_layout_desc* desc, const int32_t* topk_idx_d,
                             const int32_t* offsets_d, const int32_t* dst_row_d,
                             const int32_t* src_row_d, int64_t m_cap, void* stream, char* detail,

@@ -137,6 +137,7 @@ __device__ __forceinline__ void for_each_index(F&& f, std::integer_sequence<int,
 // They assume arguments were checked by the C ABI layer.
 struct moe_route_desc;
 struct moe_linear_desc;
+struct moe_tensor_ref;
 
 namespace moe {
 
@@ -227,6 +228,13 @@ hipError_t launch_gate_up_wgrad(const void* x_perm, const void* dgu, const int32
 hipError_t launch_down_wgrad(const void* h, const void* dy, const int32_t* offsets,
                              const int32_t* counts, int e_loc, int64_t m_cap, int I, int H,
                              void* dw2, hipStream_t s);
+size_t grad_sumsq_workspace_bytes(const moe_tensor_ref* refs, int n);
+hipError_t launch_grad_sumsq(const moe_tensor_ref* refs, int n, double* sumsq, void* ws,
+                             hipStream_t s);
+hipError_t launch_grad_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm,
+                            float* norm, hipStream_t s);
+// whether a written tensor shares memory with any other
+bool grad_clip_overlaps(const moe_tensor_ref* refs, int n);
 size_t dispatch_layout_workspace_bytes(int64_t T, int E, int ep);
 hipError_t launch_dispatch_layout(const int32_t* idx, int64_t T, int E, int k, int ep,
                                   int32_t* per_rank, int32_t* per_expert, uint8_t* in_rank,

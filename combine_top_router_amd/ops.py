@@ -8,6 +8,7 @@ raw pointers to the library, and raises ``MoEError`` on a non-OK status.
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -621,6 +622,76 @@ def grouped_down_wgrad(h, dy, offsets, counts, dw2=None):
         _ptr(h), _ptr(dy), _ptr(offsets), _ptr(counts), e_loc, m_cap, I, H, _ptr(dw2),
         _stream(h.device)))
     return dw2
+
+
+# ---------------------------------------------------------------- gradient clipping
+
+def _tensor_refs(grads, out=None):
+    """(host array of moe_tensor_ref, count, device) of contiguous GPU tensors."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"{len(grads)} gradients, {len(out)} outputs")
+    if not grads:
+        raise ValueError("no gradients")
+    dev = grads[0].device
+    words = array("q")
+    for g, o in zip(grads, out):
+        if not g.is_cuda or g.device != dev or o.device != dev:
+            raise ValueError(f"gradients and outputs must be on one GPU (got {g.device}, {o.device}, {dev})")
+        if g.dtype not in _ROWS or o.dtype != g.dtype:
+            raise TypeError(f"gradients must be bf16, fp16 or fp32, outputs alike (got {g.dtype}, {o.dtype})")
+        if not g.is_contiguous() or not o.is_contiguous():
+            raise ValueError("gradients and outputs must be contiguous")
+        if o is not g and o.shape != g.shape:
+            raise ValueError(f"output of shape {tuple(o.shape)} for a gradient of {tuple(g.shape)}")
+        # data, out, numel, then dtype and reserved in one word
+        words.extend((g.data_ptr(), o.data_ptr(), g.numel(), _ROWS[g.dtype]))
+    return words, len(grads), dev
+
+
+def _sumsq(words, n, dev, out):
+    refs = C.c_void_p(words.buffer_info()[0])
+    ws = _empty((int(lib().moe_grad_sumsq_workspace_bytes(refs, n)),), torch.uint8, dev)
+    out = _empty((1,), torch.float64, dev) if out is None else out
+    _need(out, "sumsq", torch.float64, (1,))
+    _same_device(dev, sumsq=out)
+    with torch.cuda.device(dev):
+        check("moe_grad_sumsq", lib().moe_grad_sumsq(refs, n, _ptr(out), _ptr(ws), ws.numel(),
+                                                     _stream(dev)))
+    return out
+
+
+def _clip(words, n, dev, sumsq, max_norm, norm):
+    norm = _empty((1,), torch.float32, dev) if norm is None else norm
+    _need(sumsq, "sumsq", torch.float64, (1,))
+    _need(norm, "norm", torch.float32, (1,))
+    _same_device(dev, sumsq=sumsq, norm=norm)
+    with torch.cuda.device(dev):
+        check("moe_grad_clip", lib().moe_grad_clip(
+            C.c_void_p(words.buffer_info()[0]), n, _ptr(sumsq), max_norm, _ptr(norm),
+            _stream(dev)))
+    return norm
+
+
+def grad_sumsq(grads, out=None) -> torch.Tensor:
+    """[1] float64: the sum of the squares of all elements of all gradients
+    (bf16, fp16 or fp32). Ranks that hold different parameters add these
+    before clip_grads."""
+    return _sumsq(*_tensor_refs(grads), out)
+
+
+def clip_grads(grads, sumsq: torch.Tensor, max_norm: float, out=None, norm=None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or
+    into the tensors of ``out``; returns the norm, [1] float32."""
+    return _clip(*_tensor_refs(grads, out), sumsq, max_norm, norm)
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, norm=None) -> torch.Tensor:
+    """grad_sumsq, then clip_grads with it: the norm of all gradients together, [1]
+    float32, the gradients scaled down to ``max_norm`` if it is larger."""
+    words, n, dev = _tensor_refs(grads, out)
+    return _clip(words, n, dev, _sumsq(words, n, dev, None), max_norm, norm)
 
 
 # ---------------------------------------------------------------- dedup layout

@@ -594,6 +594,45 @@ int32_t moe_route_backward(const int32_t* topk_idx_d, const float* topk_w_d,
                            int32_t top_k, float* grad_logits_d, void* stream);
 
 /*
+ * Norm of all gradients together, and clipping (what follows the weight
+ * gradients in a training step).
+ *
+ *   moe_grad_sumsq:  sumsq = sum of g^2 over every element of every tensor, in fp64
+ *   moe_grad_clip:   norm = sqrt(sumsq);  coef = min(1, max_norm / (norm + 1e-6));
+ *                    out = g * coef (fp32 product, one rounding);  norm_d = norm
+ *
+ * Two calls, so that ranks holding different parameters (expert parallelism)
+ * can add their sums in between. A norm that is not finite gives what the
+ * formula gives: coef NaN for a NaN norm, 0 for an infinite one. The order of the sum is
+ * fixed by the tensors' order and sizes. In place, with coef = 1, nothing is written.
+ *   tensors      HOST array of num_tensors descriptors, read during the call: `data` (device, aligned to
+ *                its elements; may be NULL if numel is 0), `out` (moe_grad_clip: where the scaled
+ *                tensor goes, of the same type; NULL or `data`: in place), numel, dtype MOE_ROWS_*
+ *   sumsq_d      [1] double (moe_grad_sumsq: out, moe_grad_clip: in)
+ *   norm_d       [1] float (out), or NULL
+ *   max_norm     >= 0 (infinity: no bound)
+ *   workspace_d  >= moe_grad_sumsq_workspace_bytes(...) bytes, 8-byte aligned
+ * A tensor may appear twice in moe_grad_sumsq (it counts twice); moe_grad_clip refuses
+ * tensors of which one is written and shares memory with another (MOE_ERR_ARG).
+ * Limits: 0 <= num_tensors <= 65536, 0 <= numel < 2^44. No tensors: the sum is 0.
+ */
+typedef struct moe_tensor_ref {
+  const void* data;
+  void* out;
+  int64_t numel;
+  int32_t dtype;
+  int32_t reserved; /* 0 */
+} moe_tensor_ref;
+
+size_t moe_grad_sumsq_workspace_bytes(const moe_tensor_ref* tensors, int32_t num_tensors);
+
+int32_t moe_grad_sumsq(const moe_tensor_ref* tensors, int32_t num_tensors, double* sumsq_d,
+                       void* workspace_d, size_t workspace_bytes, void* stream);
+
+int32_t moe_grad_clip(const moe_tensor_ref* tensors, int32_t num_tensors, const double* sumsq_d,
+                      float max_norm, float* norm_d, void* stream);
+
+/*
  * moe_combine_rows -- the fused restore on other row dtypes and variants.
  *
  * The fused restore runs on bf16 and on fp32 rows (DeepSpeed PR #8847,
