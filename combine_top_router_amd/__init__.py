@@ -14,4 +14,4 @@ from .ops import (  # noqa: F401
     layout_workspace_bytes, linear, linear_backward, pack_weights, permute, route,
     route_scored, route_scored_backward, validate_layout,
 )
-from .layer import MoELayer  # noqa: F401
+from .layer import MoELayer, Router  # noqa: F401

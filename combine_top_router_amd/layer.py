@@ -9,6 +9,14 @@ written), or, with ``gather=False``, the permute as its own stage:
     moe_route -> moe_layout -> moe_permute -> moe_grouped_gate_up
               -> moe_grouped_down -> moe_combine
 
+With ``gate_w`` the router projection comes first (moe_linear, fp32 logits);
+with ``router`` the scored router takes moe_route's place; with ``shared`` a
+shared expert runs beside the routed ones and its down projection takes their
+sum as its residual:
+
+    [moe_linear ->] moe_route | moe_route_scored -> ... -> moe_combine
+              [-> moe_grouped_gate_up -> moe_linear]
+
 All buffers are allocated once, at construction, for the worst case
 (``m_cap`` local rows), so a forward pass launches kernels only: no
 allocation, no host sync (the dispatch-without-waiting principle of DeepEP's
@@ -17,17 +25,36 @@ xtuner PR #2056, section "Design").
 """
 from __future__ import annotations
 
+from dataclasses import dataclass
+
 import torch
 
 from . import ops
 
 
+@dataclass
+class Router:
+    """How the layer's scored router chooses and weighs (``ops.route_scored``)."""
+
+    score: str = "sigmoid"
+    bias: torch.Tensor | None = None  # [E] fp32, steers the choice alone
+    num_groups: int = 1
+    top_groups: int = 1
+    group_rank: str = "top2"
+    renormalise: bool = True
+    scale: float = 1.0
+
+
 class MoELayer:
     def __init__(self, num_tokens: int, hidden: int, num_experts: int, top_k: int, inter: int,
                  w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, ep_size: int = 1,
-                 local_rank: int = -1, align: int = 128, gather: bool = True):
+                 local_rank: int = -1, align: int = 128, gather: bool = True,
+                 gate_w: torch.Tensor | None = None, router: Router | None = None,
+                 shared: tuple | None = None):
         """w1, w3: [E_loc, H, I] and w2: [E_loc, I, H], bf16 on the GPU (math
-        orientation); repacked once here into the GEMM's layout."""
+        orientation); repacked once here into the GEMM's layout. gate_w: the
+        router projection [E, H] bf16 (then no logits are given to the layer).
+        shared: a shared expert's (w1, w3 [H, Is], w2 [Is, H]) bf16, contiguous."""
         dev = w1.device
         self.T, self.H, self.E, self.k, self.I = num_tokens, hidden, num_experts, top_k, inter
         self.desc = ops.layout_desc(num_tokens, num_experts, top_k, ep_size, local_rank, align)
@@ -44,12 +71,41 @@ class MoELayer:
         self.h = torch.empty((self.m_cap, inter), dtype=torch.bfloat16, device=dev)
         self.y = torch.empty((self.m_cap, hidden), dtype=torch.bfloat16, device=dev)
         self.out = torch.empty((num_tokens, hidden), dtype=torch.bfloat16, device=dev)
+        self.router, self.gate_w, self.shared_w2 = router, gate_w, None
+        if gate_w is not None:
+            self.logits = torch.empty((num_tokens, num_experts), dtype=torch.float32, device=dev)
+            self.gate_ws = ops.linear_workspace(self.out, gate_w)
+        if shared is not None:
+            s1, s3, s2 = shared
+            self.shared_w1 = ops.pack_weights(s1.unsqueeze(0))
+            self.shared_w3 = ops.pack_weights(s3.unsqueeze(0))
+            self.shared_w2 = s2.t()  # [H, Is], its memory in math orientation
+            self.shared_h = torch.empty((num_tokens, s2.shape[0]), dtype=torch.bfloat16,
+                                        device=dev)
+            # one group of all the tokens
+            self.shared_off = torch.tensor([0, num_tokens], dtype=torch.int32, device=dev)
+            self.shared_cnt = torch.tensor([num_tokens], dtype=torch.int32, device=dev)
+            self.shared_ws = ops.linear_workspace(self.shared_h, self.shared_w2)
 
-    def stages(self, x: torch.Tensor, logits: torch.Tensor):
-        """The layer as (name, thunk) pairs, in order, for timing each stage."""
-        L = self.L
-        front = [
-            ("route", lambda: ops.route(logits, self.k, self.topk_idx, self.topk_w)),
+    def stages(self, x: torch.Tensor, logits: torch.Tensor | None = None):
+        """The layer as (name, thunk) pairs, in order, for timing each stage.
+        logits: the router's [T, E] fp32 (left out where the layer has gate_w)."""
+        L, r = self.L, self.router
+        if (logits is None) != (self.gate_w is not None):
+            raise ValueError("the layer takes logits, or has gate_w, and not both")
+        front = []
+        if self.gate_w is not None:
+            logits = self.logits
+            front.append(("gate", lambda: ops.linear(x, self.gate_w, out=self.logits,
+                                                     workspace=self.gate_ws)))
+        if r is None:
+            front.append(("route", lambda: ops.route(logits, self.k, self.topk_idx,
+                                                     self.topk_w)))
+        else:
+            front.append(("route", lambda: ops.route_scored(
+                logits, self.k, r.bias, r.score, r.num_groups, r.top_groups, r.group_rank,
+                r.renormalise, r.scale, self.topk_idx, self.topk_w)))
+        front += [
             ("layout", lambda: ops.layout(self.topk_idx, self.E, self.ep_size, self.local_rank,
                                           self.align, out=L)),
         ]
@@ -69,9 +125,18 @@ class MoELayer:
                                               out=self.y)),
             ("combine", lambda: ops.combine(self.y, L.dst_row, self.topk_w, out=self.out)),
         ]
+        if self.shared_w2 is not None:
+            back += [
+                ("shared_gate_up", lambda: ops.grouped_gate_up(
+                    x, self.shared_off, self.shared_cnt, self.shared_w1, self.shared_w3,
+                    out=self.shared_h)),
+                ("shared_down", lambda: ops.linear(
+                    self.shared_h, self.shared_w2, residual=self.out, out=self.out,
+                    workspace=self.shared_ws)),
+            ]
         return front + middle + back
 
-    def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, logits: torch.Tensor | None = None) -> torch.Tensor:
         for _, run in self.stages(x, logits):
             run()
         return self.out

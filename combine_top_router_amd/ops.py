@@ -385,6 +385,11 @@ def linear_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
     return int(lib().moe_linear_workspace_bytes(C.byref(_linear_desc(x, w, "none", 0, w.shape[0]))))
 
 
+def linear_workspace(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+    """A workspace for ``linear`` on operands of these shapes, to keep between calls."""
+    return _empty((max(linear_workspace_bytes(x, w), 16),), torch.uint8, x.device)
+
+
 def linear_backward_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
     """Bytes of workspace ``linear_backward`` needs on these operands."""
     return int(lib().moe_linear_backward_workspace_bytes(
