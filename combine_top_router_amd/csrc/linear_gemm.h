@@ -70,12 +70,34 @@ __device__ __forceinline__ void unpack8x16(const u32x4& v, float (&f)[8], bool f
   }
 }
 
+// e^x and 1/x by the hardware's base-2 exponential and reciprocal: within
+// 2^-22 (|x| + 2) of e^x, far inside what a 16-bit or summed fp32 value shows.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-z));
+}
+
+// The normal distribution function by Abramowitz and Stegun 7.1.26 (absolute
+// error of erfc at most 1.5e-7): erfc(x) = t (a1 + t (a2 + ...)) e^(-x^2),
+// t = 1 / (1 + p x), x >= 0. The library's erfcf took a third of the time of a
+// 1023x4096x14336 product with gelu. g receives e^(-z^2/2).
+__device__ __forceinline__ float normal_cdf(float z, float& g) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  g = __expf(-x * x);
+  const float half =
+      0.5f * g * t *
+      (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  return z < 0.f ? half : 1.f - half;
+}
+
 __device__ __forceinline__ float act_of(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? z : z * 0.f;  // NaN stays NaN
-    case MOE_ACT_SILU: return z / (1.f + expf(-z));
-    // erfc, not 1 + erf: no cancellation in the negative tail
-    case MOE_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case MOE_ACT_SILU: return z * sigmoid(z);
+    case MOE_ACT_GELU: {
+      float g;
+      return z * normal_cdf(z, g);
+    }
     default: return z;
   }
 }
@@ -84,56 +106,67 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case MOE_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-z));
+      const float s = sigmoid(z);
       return s * (1.f + z * (1.f - s));
     }
-    case MOE_ACT_GELU:
-      return 0.5f * erfcf(-0.70710678118654752f * z) +
-             z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    case MOE_ACT_GELU: {
+      float g;
+      const float c = normal_cdf(z, g);
+      return c + z * g * 0.39894228040143268f;
+    }
     default: return 1.f;
   }
 }
 
-// Columns n .. n+7 of output row m from their sums.
-__device__ __forceinline__ void finish8(const Epilogue& e, int64_t m, int64_t n, int64_t N,
-                                        float (&v)[8]) {
-  if (e.vec && n + 8 <= N) {
-    if (e.bias) {
+__device__ __forceinline__ u32x4 load8x16(const uint16_t* p) {
+  return *reinterpret_cast<const u32x4*>(p);
+}
+
+// Columns n .. n+7 of output row m from their sums v, the columns' bias and
+// the residual's values: rows that start 16-byte aligned.
+__device__ __forceinline__ void finish8(const Epilogue& e, int64_t m, int64_t n, float (&v)[8],
+                                        const float (&bias)[8], const u32x4& res) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += e.bias[n + i];
-    }
-    if (e.pre) *reinterpret_cast<u32x4*>(e.pre + m * e.ldp + n) = pack8x16(v, e.f16);
-    if (e.act != MOE_ACT_NONE) {
+  for (int i = 0; i < 8; ++i) v[i] += bias[i];
+  if (e.pre) *reinterpret_cast<u32x4*>(e.pre + m * e.ldp + n) = pack8x16(v, e.f16);
+  switch (e.act) {  // one uniform branch for the eight
+    case MOE_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], e.act);
-    }
-    if (e.res) {
-      float r[8];
-      unpack8x16(*reinterpret_cast<const u32x4*>(e.res + m * e.ldr + n), r, e.f16);
+      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], MOE_ACT_RELU);
+      break;
+    case MOE_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
-    if (e.out_f32) {
-      float* o = static_cast<float*>(e.out) + m * e.ldo + n;
-      *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(e.out) + m * e.ldo + n) =
-          pack8x16(v, e.f16);
-    }
-    return;
+      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], MOE_ACT_SILU);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], MOE_ACT_GELU);
+      break;
+    default: break;
   }
+  if (e.res) {
+    float r[8];
+    unpack8x16(res, r, e.f16);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (n + i >= N) continue;
-    float z = v[i];
-    if (e.bias) z += e.bias[n + i];
-    if (e.pre) e.pre[m * e.ldp + n + i] = to16(z, e.f16);
-    z = act_of(z, e.act);
-    if (e.res) z += from16(e.res[m * e.ldr + n + i], e.f16);
-    if (e.out_f32) static_cast<float*>(e.out)[m * e.ldo + n + i] = z;
-    else static_cast<uint16_t*>(e.out)[m * e.ldo + n + i] = to16(z, e.f16);
+    for (int i = 0; i < 8; ++i) v[i] += r[i];
   }
+  if (e.out_f32) {
+    float* o = static_cast<float*>(e.out) + m * e.ldo + n;
+    *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(e.out) + m * e.ldo + n) = pack8x16(v, e.f16);
+  }
+}
+
+// One output.
+__device__ __forceinline__ void finish1(const Epilogue& e, int64_t m, int64_t n, float z) {
+  if (e.bias) z += e.bias[n];
+  if (e.pre) e.pre[m * e.ldp + n] = to16(z, e.f16);
+  z = act_of(z, e.act);
+  if (e.res) z += from16(e.res[m * e.ldr + n], e.f16);
+  if (e.out_f32) static_cast<float*>(e.out)[m * e.ldo + n] = z;
+  else static_cast<uint16_t*>(e.out)[m * e.ldo + n] = to16(z, e.f16);
 }
 
 // Swizzle of a by-rows slice: the 16 rows that one LDS cycle reads at one
@@ -289,7 +322,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_kernel(GemmArgs g) {
   constexpr int STAGE = OpA::BYTES + OpB::BYTES, NL = OpA::LOADS + OpB::LOADS;
   constexpr int EP = 32 * TN * 32 * 4;  // a wavefront's epilogue block: 32 rows x 32 TN floats
   static_assert(TM * WM * 32 == BM && TN * WN * 32 == BN, "tile");
-  static_assert(EP * WAVES <= NS * STAGE && (TN == 1 || TN == 2 || TN == 4), "epilogue block");
+  static_assert(EP * WAVES <= NS * STAGE && (TN == 1 || TN == 2), "epilogue block");
   __shared__ __attribute__((aligned(1024))) char smem[NS * STAGE];
 
   const int tid = threadIdx.x, lane = lane_id(), wid = uniform(tid / kWave);
@@ -438,52 +471,86 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_kernel(GemmArgs g) {
 
   const int64_t m_end = min(g.M, m0 + height);
   // Epilogue, each wavefront by itself: a 32-row block goes to its own LDS
-  // part as fp32 (chunks of four columns, swizzled by row), then eight
-  // columns of a row per lane come back.
+  // part as fp32 (chunks of four columns, swizzled by row) and comes back
+  // eight columns of a row to a lane, where rows and columns allow 16-byte
+  // accesses, or one column to a lane. A lane keeps its columns for all rows,
+  // and a block's residual is fetched while the block before it is finished.
   char* ep = smem + wid * EP;
   constexpr int ECH = 8 * TN;  // 16-byte chunks of a block's row
   auto slot = [](int r, int c) {
     const int key = ECH >= 16 ? (r & 15) : ((r >> 1) & 7);
     return r * (ECH * 16) + ((c ^ key) << 4);
   };
-  // (one copy of the epilogue's code: unrolled, its many paths cost registers)
-#pragma unroll 1
-  for (int i = 0; i < TM && m0 + i * (32 * WM) < m_end; ++i) {
-    for_each_index([&](auto c_tag) {
-      constexpr int c = decltype(c_tag)::value;
-      if (c == i) {
+  constexpr int C8 = 4 * TN, RPI = 64 / C8, IT = 32 / RPI;  // rows of one pass of the wavefront
+  const int64_t nw = n0 + wn * (32 * TN);                    // the wavefront's first column
+  const bool parts = g.splits > 1;
+  const bool wide = parts || (g.e.vec && nw + 32 * TN <= g.N);
+  const int64_t n = nw + (lane % C8) * 8;
+  const int r_lane = lane / C8;
+  auto row_of = [&](int i, int it) { return m0 + (i * WM + wm) * 32 + it * RPI + r_lane; };
+  float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const bool has_res = wide && !parts && g.e.res;
+  u32x4 res[IT];
+  auto fetch = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+    for (int it = 0; it < IT; ++it) {
+      const int64_t m = row_of(i, it);
+      if (m < m_end) res[it] = load8x16(g.e.res + m * g.e.ldr + n);
+    }
+  };
+  if (wide && !parts && g.e.bias) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4*>(ep + slot(lane & 31, j * 8 + 2 * q + (lane >> 5))) =
-                f32x4{acc[c][j][4 * q], acc[c][j][4 * q + 1], acc[c][j][4 * q + 2],
-                      acc[c][j][4 * q + 3]};
-      }
-    }, std::make_integer_sequence<int, TM>{});
+    for (int q = 0; q < 8; ++q) bias[q] = g.e.bias[n + q];
+  }
+  if (has_res) fetch(0);
+  for_each_index([&](auto i_tag) {
+    constexpr int i = decltype(i_tag)::value;
+    if (m0 + i * (32 * WM) >= m_end) return;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(ep + slot(lane & 31, j * 8 + 2 * q + (lane >> 5))) =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                  acc[i][j][4 * q + 3]};
     // one wavefront's LDS accesses complete in order; the fence keeps the compiler's
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    constexpr int C8 = 4 * TN;  // groups of eight columns
-#pragma unroll 1
-    for (int it = 0; it < 32 * C8 / 64; ++it) {
-      const int c = it * 64 + lane, r = c / C8, c8 = c % C8;
-      const f32x4 x = *reinterpret_cast<const f32x4*>(ep + slot(r, 2 * c8));
-      const f32x4 y = *reinterpret_cast<const f32x4*>(ep + slot(r, 2 * c8 + 1));
-      const int64_t m = m0 + (i * WM + wm) * 32 + r;
-      const int64_t n = n0 + wn * (32 * TN) + c8 * 8;
-      if (m < m_end && n < g.N) {
-        if (g.splits > 1) {
-          float* p = g.part + (int64_t(split) * g.M + m) * g.nw + n;
-          *reinterpret_cast<f32x4*>(p) = x;
-          *reinterpret_cast<f32x4*>(p + 4) = y;
-        } else {
-          float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-          finish8(g.e, m, n, g.N, v);
+    if (wide) {
+      u32x4 now[IT];
+#pragma unroll
+      for (int it = 0; it < IT; ++it) now[it] = res[it];
+      if (has_res && i + 1 < TM) fetch(i + 1);
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int r = it * RPI + r_lane;
+        const int64_t m = row_of(i, it);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(ep + slot(r, 2 * (lane % C8)));
+        const f32x4 y = *reinterpret_cast<const f32x4*>(ep + slot(r, 2 * (lane % C8) + 1));
+        if (m < m_end && n < g.N) {
+          if (parts) {
+            float* p = g.part + (int64_t(split) * g.M + m) * g.nw + n;
+            *reinterpret_cast<f32x4*>(p) = x;
+            *reinterpret_cast<f32x4*>(p + 4) = y;
+          } else {
+            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            finish8(g.e, m, n, v, bias, now[it]);
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);  // one pass's values at a time in registers
+      }
+    } else {
+      constexpr int COLS = 32 * TN < 64 ? 32 * TN : 64;  // columns side by side
+      const int rl = lane / COLS;
+#pragma unroll 4
+      for (int r0 = 0; r0 < 32; r0 += 64 / COLS) {
+        const int r = r0 + rl, c = lane % COLS;
+        const int64_t m = m0 + (i * WM + wm) * 32 + r;
+        const float z = *reinterpret_cast<const float*>(ep + slot(r, c >> 2) + (c & 3) * 4);
+        if (m < m_end && nw + c < g.N) finish1(g.e, m, nw + c, z);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
+  }, std::make_integer_sequence<int, TM>{});
 }
 
 // The sums of the splits, in order, and the epilogue: eight columns a thread (64 threads
@@ -512,7 +579,16 @@ __global__ __launch_bounds__(64) void linear_join_kernel(GemmArgs g) {
         for (int i = 0; i < 4; ++i) v[i] += x[u][i], v[4 + i] += y[u][i];
       }
   }
-  finish8(g.e, m, n, g.N, v);
+  if (g.e.vec && n + 8 <= g.N) {
+    float bias[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias[i] = g.e.bias ? g.e.bias[n + i] : 0.f;
+    finish8(g.e, m, n, v, bias, g.e.res ? load8x16(g.e.res + m * g.e.ldr + n) : u32x4{0, 0, 0, 0});
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (n + i < g.N) finish1(g.e, m, n + i, v[i]);
+  }
 }
 
 }  // namespace
