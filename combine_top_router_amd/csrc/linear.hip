@@ -32,6 +32,7 @@
 //  * Products of 16-bit values are exact in fp32 and summed in fp32; the
 //    epilogue is fp32, with one rounding per stored value.
 #include <algorithm>
+#include <iterator>
 
 #include "linear_gemm.h"
 
@@ -119,55 +120,74 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int b
 
 constexpr int BK = 64;  // reduction indexes of a slice
 
-// A tile shape with what one workgroup takes, in microseconds, measured over
-// products of 1 to 65536 rows and columns: a slice alone on its compute unit,
-// a slice beside a second workgroup (per_cu 2), and the beginning and end.
+// A tile shape with what its workgroups take, in microseconds: a slice on a
+// quiet chip, a slice where a second workgroup shares the compute unit (per_cu
+// 2), and a workgroup's beginning and end without its stores.
 struct Tile {
   int bm, bn, per_cu;
-  double slice, slice_shared, fixed;
+  double slice, shared, fixed;
 };
 constexpr Tile kTiles[] = {
-    {256, 256, 1, 1.04, 0.0, 4.5},  {128, 256, 1, 0.74, 0.0, 3.5}, {128, 128, 2, 0.51, 1.04, 2.7},
-    {64, 128, 2, 0.33, 0.72, 2.3}, {64, 64, 2, 0.27, 0.52, 1.7},
+    {256, 256, 1, 0.87, 0.0, 2.5},  {128, 256, 1, 0.55, 0.0, 2.9}, {128, 128, 2, 0.45, 1.35, 2.4},
+    {64, 128, 2, 0.30, 0.89, 2.4},  {64, 64, 2, 0.225, 0.59, 2.0}, {128, 128, 1, 0.375, 0.0, 2.5},
 };
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
 
 struct Plan {
-  int tile, splits, per_split;
+  int tile, splits, per_split, halved;
   int64_t part_bytes;
 };
 
 // Tile and split of one product, from its sizes alone: the least estimated
-// time. Large products take the largest tile (fewest bytes through LDS per
-// product: 4096x14336x4096 in 349 us against 402-457 with 128x128), few
-// outputs small tiles and a split reduction (16x7168x256: 64x64 in 8 parts
-// 12 us, whole 34 us). Over 500 sizes the choice was within 3 % of
-// the best of these tiles and splits on average.
+// time. Rounds of workgroups over the chip, each of its slices (slower the
+// more of the chip works: clock and memory) and its stores; at least
+// the memory's time for the operands; for a split the second launch. The
+// figures are a fit to 25000 timings of these tiles and splits on 800
+// products of 1 to 65536 rows and 8 to 16384 columns and terms; on them the choice is 1.1 % slower
+// than the best on average and 25 % at worst. Examples: 4096x14336x4096 takes
+// 256x256 (349 us, 128x128 402-457 us), 16x7168x256 64x64 in 16 parts (9 us;
+// whole, 34 us), 8192x256x7168 128x128 (57 us, 256x256 70 us).
 Plan plan_product(int64_t M, int64_t N, int64_t K) {
-  const int cus = device_cu_count();
+  const int64_t cus = device_cu_count();
   const int64_t all = std::max<int64_t>(1, (K + BK - 1) / BK);
-  const double mem = (double(M) * K + double(N) * K + double(M) * N) * 2.0 / 5.2e6;  // at 5.2 TB/s
-  const double out = double(M) * double((N + 7) / 8 * 8) * 4.0;
-  Plan best{0, 1, static_cast<int>(all), 0};
-  double best_t = 1e30;
-  for (int t = 0; t < 5; ++t) {
+  const int64_t nw = (N + 7) / 8 * 8;
+  const double mem = (double(M) * K + double(N) * K + double(M) * N) * 2.0 / 5.75e6;
+  Plan best{0, 1, static_cast<int>(all), 0, 0};
+  double best_t = 1e300;
+  for (int t = 0; t < int(std::size(kTiles)); ++t) {
     const Tile& c = kTiles[t];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     for (const int want : kSplits) {
       if (want > 1 && want * 2 > all) break;
-      const int64_t per = (all + want - 1) / want, s = (all + per - 1) / per;
-      const int64_t groups = tiles * s, slots = int64_t(cus) * c.per_cu;
-      const int64_t full = groups / slots, rest = groups % slots;
-      const double alone = double(per) * c.slice + c.fixed;
-      const double shared = c.per_cu == 2 ? double(per) * c.slice_shared + c.fixed : alone;
-      double time = double(full) * shared + (rest == 0 ? 0.0 : rest <= cus ? alone : shared);
+      const int64_t per = (all + want - 1) / want, s = (all + per - 1) / per, groups = tiles * s;
+      const double out = double(std::min<int64_t>(c.bm, M)) * double(std::min<int64_t>(c.bn, N)) *
+                         (s > 1 ? 4.0 : 2.0) / 3.45e6;  // one workgroup's stores, us
+      const int64_t slots = cus * c.per_cu, full = groups / slots, rest = groups % slots;
+      const double load = double(rest) / double(cus), p = double(per);
+      double time;
+      int halved = 0;
+      if (c.per_cu == 1) {
+        const double round = p * c.slice * 1.7 + c.fixed + double(cus) * out;
+        time = double(full) * round;
+        // A last round that fills at most half of an XCD's compute units: its tiles
+        // are cut in two (8192x2048x7168, 3.5 rounds: 230 -> 218 us).
+        const int64_t last = groups / 8 % (cus / 8) + (groups % 8 ? 1 : 0);
+        if (t == 0 && s == 1 && full > 0 && rest > 0 && last <= cus / 16)
+          halved = static_cast<int>(last), time += 0.83 * round;
+        else if (rest > 0)
+          time += p * c.slice * (1.0 + 0.7 * load) + c.fixed + double(rest) * out;
+      } else {
+        time = double(full) * (std::max(p * c.shared, double(slots) * out) + c.fixed);
+        if (rest > cus)
+          time += p * c.shared * (1.0 - 0.25 * (2.0 - load)) + c.fixed + 0.5 * double(rest) * out;
+        else if (rest > 0)
+          time += p * c.slice * (1.0 + 0.5 * load) + c.fixed + double(rest) * out;
+      }
       time = std::max(time, mem);
-      // the second launch: its parts' loads, and the parts written and read
-      if (s > 1) time += 0.8 + 0.07 * double(s) + double(s) * out / 2.4e6;
+      if (s > 1) time += 1.4 + 0.07 * double(s) + double(s) * double(M) * double(nw) * 4.0 / 5.4e6;
       if (time < best_t) {
         best_t = time;
-        best = {t, static_cast<int>(s), static_cast<int>(per),
-                s > 1 ? s * M * ((N + 7) / 8 * 8) * 4 : 0};
+        best = {t, static_cast<int>(s), static_cast<int>(per), halved, s > 1 ? s * M * nw * 4 : 0};
       }
     }
   }
@@ -179,10 +199,11 @@ void launch_product(const GemmArgs& g, int tile, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(int64_t(g.tiles_m) * g.tiles_n * g.splits + 8 * g.halved));
   switch (tile) {
     case 0: linear_kernel<F16, AC, BC, 256, 256, BK, 2, 4, 2, 2><<<grid, 512, 0, s>>>(g); break;
-    case 1: linear_kernel<F16, AC, BC, 128, 256, BK, 2, 4, 2, 2><<<grid, 512, 0, s>>>(g); break;
+    case 1: linear_kernel<F16, AC, BC, 128, 256, BK, 2, 4, 3, 2><<<grid, 512, 0, s>>>(g); break;
     case 2: linear_kernel<F16, AC, BC, 128, 128, BK, 2, 2, 2, 2><<<grid, 256, 0, s>>>(g); break;
     case 3: linear_kernel<F16, AC, BC, 64, 128, BK, 1, 4, 3, 2><<<grid, 256, 0, s>>>(g); break;
-    default: linear_kernel<F16, AC, BC, 64, 64, BK, 2, 2, 4, 2><<<grid, 256, 0, s>>>(g); break;
+    case 4: linear_kernel<F16, AC, BC, 64, 64, BK, 2, 2, 4, 2><<<grid, 256, 0, s>>>(g); break;
+    default: linear_kernel<F16, AC, BC, 128, 128, BK, 2, 4, 4, 2><<<grid, 512, 0, s>>>(g); break;
   }
 }
 
@@ -192,15 +213,8 @@ hipError_t product(GemmArgs g, bool a_cols, bool b_cols, void* ws, hipStream_t s
   const Tile& c = kTiles[p.tile];
   g.tiles_m = static_cast<int>((g.M + c.bm - 1) / c.bm);
   g.tiles_n = static_cast<int>((g.N + c.bn - 1) / c.bn);
-  g.splits = p.splits, g.per_split = p.per_split;
+  g.splits = p.splits, g.per_split = p.per_split, g.halved = p.halved;
   g.part = static_cast<float*>(ws), g.nw = (g.N + 7) / 8 * 8;
-  // A last round that fills at most half of an XCD's compute units: its tiles
-  // are cut in two (8192x2048x7168, 3.5 rounds: 230 -> 218 us).
-  const int per_xcd = device_cu_count() / 8 * c.per_cu, tiles = g.tiles_m * g.tiles_n;
-  if (p.tile == 0 && g.splits == 1 && tiles / 8 >= per_xcd) {
-    const int last = tiles / 8 % per_xcd + (tiles % 8 ? 1 : 0);
-    if (last <= per_xcd / 2) g.halved = last;
-  }
   if (g.e.f16) {
     if (a_cols) launch_product<true, true, true>(g, p.tile, s);
     else if (b_cols) launch_product<true, false, true>(g, p.tile, s);

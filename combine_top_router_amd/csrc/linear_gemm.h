@@ -122,51 +122,87 @@ __device__ __forceinline__ u32x4 load8x16(const uint16_t* p) {
   return *reinterpret_cast<const u32x4*>(p);
 }
 
-// Columns n .. n+7 of output row m from their sums v, the columns' bias and
-// the residual's values: rows that start 16-byte aligned.
-__device__ __forceinline__ void finish8(const Epilogue& e, int64_t m, int64_t n, float (&v)[8],
-                                        const float (&bias)[8], const u32x4& res) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] += bias[i];
-  if (e.pre) *reinterpret_cast<u32x4*>(e.pre + m * e.ldp + n) = pack8x16(v, e.f16);
-  switch (e.act) {  // one uniform branch for the eight
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+  switch (act) {  // one uniform branch for all of them
     case MOE_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], MOE_ACT_RELU);
+      for (int i = 0; i < N; ++i) v[i] = act_of(v[i], MOE_ACT_RELU);
       break;
     case MOE_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], MOE_ACT_SILU);
+      for (int i = 0; i < N; ++i) v[i] = act_of(v[i], MOE_ACT_SILU);
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = act_of(v[i], MOE_ACT_GELU);
+      for (int i = 0; i < N; ++i) v[i] = act_of(v[i], MOE_ACT_GELU);
       break;
     default: break;
   }
-  if (e.res) {
-    float r[8];
-    unpack8x16(res, r, e.f16);
+}
+
+// Where a block of outputs begins: offsets inside it fit 32 bits.
+struct Block {
+  char* out;
+  const uint16_t* res;
+  uint16_t* pre;
+  int ldo, ldr, ldp;
+  __device__ __forceinline__ Block(const Epilogue& e, int64_t m, int64_t n)
+      : out(static_cast<char*>(e.out) + (m * e.ldo + n) * (e.out_f32 ? 4 : 2)),
+        res(e.res ? e.res + m * e.ldr + n : nullptr), pre(e.pre ? e.pre + m * e.ldp + n : nullptr),
+        ldo(int(e.ldo)), ldr(int(e.ldr)), ldp(int(e.ldp)) {}
+};
+
+// Columns c .. c+7 of a block's row r from their sums v, the columns' bias and
+// the residual's values: rows that start 16-byte aligned.
+__device__ __forceinline__ void finish8(const Epilogue& e, const Block& b, int r, int c,
+                                        float (&v)[8], const float (&bias)[8], const u32x4& res) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
+  for (int i = 0; i < 8; ++i) v[i] += bias[i];
+  if (e.pre) *reinterpret_cast<u32x4*>(b.pre + (r * b.ldp + c)) = pack8x16(v, e.f16);
+  act_all(v, e.act);
+  if (e.res) {
+    float x[8];
+    unpack8x16(res, x, e.f16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
   }
   if (e.out_f32) {
-    float* o = static_cast<float*>(e.out) + m * e.ldo + n;
+    float* o = reinterpret_cast<float*>(b.out) + (r * b.ldo + c);
     *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
     *reinterpret_cast<f32x4*>(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
   } else {
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(e.out) + m * e.ldo + n) = pack8x16(v, e.f16);
+    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(b.out) + (r * b.ldo + c)) =
+        pack8x16(v, e.f16);
   }
 }
 
-// One output.
-__device__ __forceinline__ void finish1(const Epilogue& e, int64_t m, int64_t n, float z) {
-  if (e.bias) z += e.bias[n];
-  if (e.pre) e.pre[m * e.ldp + n] = to16(z, e.f16);
-  z = act_of(z, e.act);
-  if (e.res) z += from16(e.res[m * e.ldr + n], e.f16);
-  if (e.out_f32) static_cast<float*>(e.out)[m * e.ldo + n] = z;
-  else static_cast<uint16_t*>(e.out)[m * e.ldo + n] = to16(z, e.f16);
+// Column c of the rows r, r + step, ... of a block, from their sums v, as far as
+// they lie before `end`: rows of any alignment.
+template <int N>
+__device__ __forceinline__ void finish_column(const Epilogue& e, const Block& b, int r, int step,
+                                              int end, int c, float (&v)[N], float bias) {
+  uint16_t x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = e.res && r + i * step < end ? b.res[(r + i * step) * b.ldr + c] : 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] += bias;
+  if (e.pre) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (r + i * step < end) b.pre[(r + i * step) * b.ldp + c] = to16(v[i], e.f16);
+  }
+  act_all(v, e.act);
+  if (e.res) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += from16(x[i], e.f16);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (r + i * step >= end) continue;
+    if (e.out_f32) reinterpret_cast<float*>(b.out)[(r + i * step) * b.ldo + c] = v[i];
+    else reinterpret_cast<uint16_t*>(b.out)[(r + i * step) * b.ldo + c] = to16(v[i], e.f16);
+  }
 }
 
 // Swizzle of a by-rows slice: the 16 rows that one LDS cycle reads at one
@@ -484,28 +520,31 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_kernel(GemmArgs g) {
   constexpr int C8 = 4 * TN, RPI = 64 / C8, IT = 32 / RPI;  // rows of one pass of the wavefront
   const int64_t nw = n0 + wn * (32 * TN);                    // the wavefront's first column
   const bool parts = g.splits > 1;
-  const bool wide = parts || (g.e.vec && nw + 32 * TN <= g.N);
-  const int64_t n = nw + (lane % C8) * 8;
-  const int r_lane = lane / C8;
-  auto row_of = [&](int i, int it) { return m0 + (i * WM + wm) * 32 + it * RPI + r_lane; };
+  const bool wide = parts || (g.e.vec && (nw + 32 * TN <= g.N || g.N % 8 == 0));
+  const int cols = static_cast<int>(min(int64_t(32 * TN), g.N - nw));  // may be none
+  const int c0 = (lane % C8) * 8;  // wide: all eight columns exist, or none
+  const int r0 = lane / C8;
+  auto block_row = [&](int i) { return m0 + (i * WM + wm) * 32; };
   float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const bool has_res = wide && !parts && g.e.res;
   u32x4 res[IT];
   auto fetch = [&](int i) __attribute__((always_inline)) {
+    const uint16_t* p = g.e.res + block_row(i) * g.e.ldr + nw;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
-      const int64_t m = row_of(i, it);
-      if (m < m_end) res[it] = load8x16(g.e.res + m * g.e.ldr + n);
+      const int r = it * RPI + r0;
+      if (block_row(i) + r < m_end && c0 < cols) res[it] = load8x16(p + (r * int(g.e.ldr) + c0));
     }
   };
-  if (wide && !parts && g.e.bias) {
+  if (wide && !parts && g.e.bias && c0 < cols) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) bias[q] = g.e.bias[n + q];
+    for (int q = 0; q < 8; ++q) bias[q] = g.e.bias[nw + c0 + q];
   }
   if (has_res) fetch(0);
   for_each_index([&](auto i_tag) {
     constexpr int i = decltype(i_tag)::value;
-    if (m0 + i * (32 * WM) >= m_end) return;
+    const int64_t mb = block_row(i);
+    if (mb >= m_end || cols <= 0) return;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -515,38 +554,43 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_kernel(GemmArgs g) {
                   acc[i][j][4 * q + 3]};
     // one wavefront's LDS accesses complete in order; the fence keeps the compiler's
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int rows = static_cast<int>(min(int64_t(32), m_end - mb));
     if (wide) {
       u32x4 now[IT];
 #pragma unroll
       for (int it = 0; it < IT; ++it) now[it] = res[it];
       if (has_res && i + 1 < TM) fetch(i + 1);
+      const Block b(g.e, mb, nw);
+      float* part = g.part + (int64_t(split) * g.M + mb) * g.nw + nw;
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int r = it * RPI + r_lane;
-        const int64_t m = row_of(i, it);
+        const int r = it * RPI + r0;
         const f32x4 x = *reinterpret_cast<const f32x4*>(ep + slot(r, 2 * (lane % C8)));
         const f32x4 y = *reinterpret_cast<const f32x4*>(ep + slot(r, 2 * (lane % C8) + 1));
-        if (m < m_end && n < g.N) {
+        if (r < rows && c0 < cols) {
           if (parts) {
-            float* p = g.part + (int64_t(split) * g.M + m) * g.nw + n;
+            float* p = part + (r * int(g.nw) + c0);
             *reinterpret_cast<f32x4*>(p) = x;
             *reinterpret_cast<f32x4*>(p + 4) = y;
           } else {
             float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            finish8(g.e, m, n, v, bias, now[it]);
+            finish8(g.e, b, r, c0, v, bias, now[it]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);  // one pass's values at a time in registers
       }
     } else {
-      constexpr int COLS = 32 * TN < 64 ? 32 * TN : 64;  // columns side by side
-      const int rl = lane / COLS;
-#pragma unroll 4
-      for (int r0 = 0; r0 < 32; r0 += 64 / COLS) {
-        const int r = r0 + rl, c = lane % COLS;
-        const int64_t m = m0 + (i * WM + wm) * 32 + r;
-        const float z = *reinterpret_cast<const float*>(ep + slot(r, c >> 2) + (c & 3) * 4);
-        if (m < m_end && nw + c < g.N) finish1(g.e, m, nw + c, z);
+      constexpr int ACROSS = 32 * TN, STEP = 64 / ACROSS, BATCH = 8;
+      const int c = lane % ACROSS;
+      const Block b(g.e, mb, nw);
+      const float b1 = c < cols && g.e.bias ? g.e.bias[nw + c] : 0.f;
+#pragma unroll 1
+      for (int r = lane / ACROSS; r < 32; r += STEP * BATCH) {
+        float z[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+          z[u] = *reinterpret_cast<const float*>(ep + slot(r + u * STEP, c >> 2) + (c & 3) * 4);
+        finish_column(g.e, b, r, STEP, c < cols ? rows : 0, c, z, b1);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -579,15 +623,18 @@ __global__ __launch_bounds__(64) void linear_join_kernel(GemmArgs g) {
         for (int i = 0; i < 4; ++i) v[i] += x[u][i], v[4 + i] += y[u][i];
       }
   }
+  const Block b(g.e, m, n);
   if (g.e.vec && n + 8 <= g.N) {
     float bias[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) bias[i] = g.e.bias ? g.e.bias[n + i] : 0.f;
-    finish8(g.e, m, n, v, bias, g.e.res ? load8x16(g.e.res + m * g.e.ldr + n) : u32x4{0, 0, 0, 0});
+    finish8(g.e, b, 0, 0, v, bias, b.res ? load8x16(b.res) : u32x4{0, 0, 0, 0});
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (n + i < g.N) finish1(g.e, m, n + i, v[i]);
+    for (int i = 0; i < 8; ++i) {
+      float one[1] = {v[i]};
+      if (n + i < g.N) finish_column(g.e, b, 0, 1, 1, i, one, g.e.bias ? g.e.bias[n + i] : 0.f);
+    }
   }
 }
 

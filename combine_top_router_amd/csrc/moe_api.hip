@@ -488,9 +488,13 @@ int32_t moe_combine_rows(const void* y_d, int32_t row_dtype, int64_t y_rows,
                                             num_tokens, hidden, top_k, out_d, as_stream(stream)));
 }
 
+// rows of `cols` elements, `ld` apart: a tile's offsets have to fit 32 bits
+static bool row_stride_ok(int64_t ld, int64_t cols) {
+  return ld >= cols && ld <= (int64_t(1) << 21);
+}
+
 static int32_t linear_desc_status(const moe_linear_desc* d) {
   constexpr int32_t kDim = 1 << 20;
-  constexpr int64_t kStride = int64_t(1) << 21;
   if (!d || d->rows < 0 || d->rows >= (int64_t(1) << 31) || d->inner < 8 || d->inner > kDim ||
       d->cols < 1 || d->cols > kDim)
     return MOE_ERR_ARG;
@@ -499,9 +503,9 @@ static int32_t linear_desc_status(const moe_linear_desc* d) {
   if (d->y_f32 != 0 && d->y_f32 != 1) return MOE_ERR_ARG;
   if (d->dtype != MOE_ROWS_BF16 && d->dtype != MOE_ROWS_F16) return MOE_ERR_UNSUPPORTED;
   const bool nk = d->w_order == MOE_W_NK;
-  if (d->ldx < d->inner || d->ldw < (nk ? d->inner : d->cols) || d->ldy < d->cols)
+  if (!row_stride_ok(d->ldx, d->inner) || !row_stride_ok(d->ldw, nk ? d->inner : d->cols) ||
+      !row_stride_ok(d->ldy, d->cols))
     return MOE_ERR_ARG;
-  if (d->ldx > kStride || d->ldw > kStride || d->ldy > kStride) return MOE_ERR_ARG;
   if (d->inner % 8 || d->ldx % 8 || d->ldw % 8 || (!nk && d->cols % 8))
     return MOE_ERR_UNSUPPORTED;
   // a launch's workgroups (of at least 32 x 128 outputs) are counted in 32 bits
@@ -528,7 +532,8 @@ int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d
   const int32_t st = linear_desc_status(desc);
   if (st != MOE_OK || desc->rows == 0) return st;
   if (!x_d || !w_d || !y_d || !aligned16(x_d) || !aligned16(w_d)) return MOE_ERR_ARG;
-  if ((residual_d && desc->ldr < desc->cols) || (pre_d && desc->ldp < desc->cols))
+  if ((residual_d && !row_stride_ok(desc->ldr, desc->cols)) ||
+      (pre_d && !row_stride_ok(desc->ldp, desc->cols)))
     return MOE_ERR_ARG;
   if (pre_d && (pre_d == y_d || pre_d == residual_d)) return MOE_ERR_ARG;
   if (residual_d == y_d && (desc->y_f32 || desc->ldr != desc->ldy)) return MOE_ERR_ARG;
@@ -546,7 +551,8 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
   if (st != MOE_OK || (!dx_d && !dw_d && !dbias_d)) return st;
   if (desc->rows > 0) {
     if (!dy_d) return MOE_ERR_ARG;
-    if (desc->act != MOE_ACT_NONE && (!pre_d || desc->ldp < desc->cols)) return MOE_ERR_ARG;
+    if (desc->act != MOE_ACT_NONE && (!pre_d || !row_stride_ok(desc->ldp, desc->cols)))
+      return MOE_ERR_ARG;
     if (dx_d && (!w_d || !aligned16(w_d))) return MOE_ERR_ARG;
     if (dw_d && (!x_d || !aligned16(x_d))) return MOE_ERR_ARG;
   }

@@ -128,6 +128,42 @@ def test_backward(shape, dtype):
             _backward(gen, M, K, N, dtype, order, act, f32=(i + j) % 2 == 1, bias=j < 3)
 
 
+@pytest.mark.parametrize("shape", [(4361, 2056, 4360), (6149, 2056, 6148), (1030, 2056, 4104),
+                                   (1000, 4104, 2056), (2100, 4360, 4104)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_large_tiles_against_float64_on_the_device(shape):
+    """The largest tiles, halved ones among them: the float64 products on the GPU."""
+    M, K, N = shape
+    gen = torch.Generator("cuda").manual_seed(K)
+    for order in _orders(N):
+        for dtype in (BF, FP):
+            print("CASE large", shape, order, dtype, flush=True)
+            u = HALF_STEP[dtype]
+            x = _matrix(gen, M, K, dtype)
+            w = _matrix(gen, N, K, dtype, 0, K ** -0.5) if order == "nk" else \
+                _matrix(gen, K, N, dtype, 0, K ** -0.5).t()
+            r, dy = _matrix(gen, M, N, dtype), _matrix(gen, M, N, dtype)
+            b = torch.randn((N,), generator=gen, device="cuda")
+            X, W, D = x.double(), w.double(), dy.double()
+            XA, WA, DA = X.abs(), W.abs(), D.abs()
+
+            def near(got, want, e, half):
+                err = (got.double() - want).abs()
+                assert bool((err <= e + half * (want.abs() + e) + TINY[got.dtype]).all())
+
+            y = ops.linear(x, w, b, "none", r)
+            z = X @ W.t() + b.double()
+            e = (K + 160) * 2.0 ** -23 * (XA @ WA.t()) + 2.0 ** -22 * (z.abs() + r.double().abs())
+            near(y, z + r.double(), e, u)
+            y = ops.linear(x, w, out_dtype=torch.float32)
+            near(y, X @ W.t(), (K + 160) * 2.0 ** -23 * (XA @ WA.t()), 2.0 ** -24)
+            # dy is read as it is where its rows allow, or copied exactly
+            dx, dw, db = ops.linear_backward(dy, x, w, want_dbias=True)
+            near(dx, D @ W, (N + 160) * 2.0 ** -23 * (DA @ WA), u)
+            near(dw, D.t() @ X, (M + 160) * 2.0 ** -23 * (DA.t() @ XA), u)
+            near(db, D.sum(dim=0), (M / 8 + 16) * 2.0 ** -24 * DA.sum(dim=0), 2.0 ** -24)
+
+
 @pytest.mark.parametrize("pad", [8, 24])
 @pytest.mark.parametrize("shape", [(37, 72, 40), (300, 200, 264), (40, 4096, 128), (600, 64, 16)],
                          ids=lambda s: "x".join(map(str, s)))
