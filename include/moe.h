@@ -92,9 +92,9 @@ int32_t moe_route(const float* logits_d, int64_t num_tokens, int32_t num_experts
  *   the k experts of those groups with the largest v, in descending order
  *   w_j = scale * s_j, or with renormalise scale * s_j / (sum of s over the k selected)
  *
- * ties to the lower index. Scores, ranks and weights are formed in fp64, so the
- * choice does not depend on how an fp32 exponential rounds; the weights are
- * rounded once. A NaN logit counts as -inf, +inf as the largest finite fp32; an
+ * ties to the lower index. The choice is the one that fp64 scores, values and
+ * ranks give: it does not depend on how an fp32 exponential rounds. The weights
+ * are formed in fp32 (fp64 where a selected score would underflow). A NaN logit counts as -inf, +inf as the largest finite fp32; an
  * expert at -inf has score 0 and stays selectable. v = NaN (from the bias)
  * counts as -inf. Renormalised weights whose sum is 0 are all 0.
  *

@@ -20,6 +20,9 @@ SHAPES = [
     (65, 160, 6, 8, 3), (129, 256, 8, 8, 4), (17, 66, 5, 6, 2), (40, 18, 3, 9, 4),
     (31, 256, 16, 1, 1), (50, 384, 8, 1, 1), (9, 1024, 16, 64, 3), (5, 1023, 16, 33, 2),
     (7, 1000, 12, 5, 2), (21, 64, 8, 64, 9), (6, 16, 16, 2, 2), (1000, 128, 8, 1, 1),
+    # more tokens than get a wavefront each
+    (2100, 256, 8, 8, 4), (2500, 128, 8, 1, 1), (2200, 60, 4, 6, 2), (3001, 33, 7, 1, 1),
+    (2057, 500, 16, 4, 3),
 ]
 
 
@@ -38,7 +41,24 @@ def _check(logits, k, bias, score, groups, top_groups, rank, renorm, scale):
     want_idx, want_w = oscored.route(ln, k, None if bias is None else bias.cpu().numpy(), score,
                                      groups, top_groups, rank, renorm, np.float32(scale).item())
     assert (idx.cpu().numpy() == want_idx).all()
-    _same(w, want_w)
+    # A weight in fp32: expf (2 half steps), 1 + e and its reciprocal (2), a sum across at
+    # most 64 lanes (6, on top of its terms' 4), the quotient and the scale (2): 16 half steps.
+    # The softmax's arguments are rounded differences, |l - max| half steps for the term
+    # and, weighted by the terms, for the sum, which takes up to 38 additions if over all experts.
+    half_steps = 16.0
+    if score == "softmax":
+        l = oscored._clean(ln)
+        sel = np.take_along_axis(l, want_idx.astype(np.int64), axis=1)
+        with np.errstate(invalid="ignore"):
+            far = np.where(sel == -np.inf, 0.0,
+                           np.abs(sel - (sel if renorm else l).max(axis=1, keepdims=True)))
+            every = np.where(l == -np.inf, 0.0, np.abs(l - l.max(axis=1, keepdims=True)))
+        p = oscored.scores(ln, score)
+        mean = (p * np.where(p > 0, every, 0.0)).sum(axis=1, keepdims=True)
+        # where fp64 takes over (|l - max| above 80) nothing of this is lost: 80 at most
+        half_steps = 16 + np.minimum(far, 80) + \
+            (np.minimum(far, 80).max(axis=1, keepdims=True) if renorm else 38 + mean)
+    _same(w, want_w, np.abs(want_w) * half_steps * U)
     return idx
 
 
