@@ -147,8 +147,7 @@ struct Plan {
 // than the best on average and 25 % at worst. Examples: 4096x14336x4096 takes
 // 256x256 (349 us, 128x128 402-457 us), 16x7168x256 64x64 in 16 parts (9 us;
 // whole, 34 us), 8192x256x7168 128x128 (57 us, 256x256 70 us).
-Plan plan_product(int64_t M, int64_t N, int64_t K) {
-  const int64_t cus = device_cu_count();
+Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t cus) {
   const int64_t all = std::max<int64_t>(1, (K + BK - 1) / BK);
   const int64_t nw = (N + 7) / 8 * 8;
   const double mem = (double(M) * K + double(N) * K + double(M) * N) * 2.0 / 5.75e6;
@@ -192,6 +191,25 @@ Plan plan_product(int64_t M, int64_t N, int64_t K) {
     }
   }
   return best;
+}
+
+// The last few plans of this thread: a call asks for its plan several times over
+// (its workspace, the check of it, the launch), and making one takes 2 us.
+Plan plan_product(int64_t M, int64_t N, int64_t K) {
+  struct Known {
+    int64_t M, N, K, cus;
+    Plan p;
+  };
+  constexpr int kKnown = 8;
+  thread_local Known known[kKnown] = {};
+  thread_local int next = 0;
+  const int64_t cus = device_cu_count();
+  for (const Known& k : known)
+    if (k.cus == cus && k.M == M && k.N == N && k.K == K) return k.p;
+  const Plan p = make_plan(M, N, K, cus);
+  known[next] = {M, N, K, cus, p};
+  next = (next + 1) % kKnown;
+  return p;
 }
 
 template <bool F16, bool AC, bool BC>

@@ -69,10 +69,40 @@ def _one_of(table: dict, key, name: str) -> int:
     return table[key]
 
 
-def _same_device(dev: torch.device, **tensors):
-    for name, t in tensors.items():
+def _same_device(dev: torch.device, *tensors):
+    for t in tensors:
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+            raise ValueError(f"all tensors must be on {dev} (got {t.device})")
+
+
+def _out(t, name: str, dtype, shape, dev: torch.device) -> torch.Tensor:
+    """The output tensor ``t``, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, shape)
+    _same_device(dev, t)
+    return t
+
+
+def _at(t):
+    """Address of a tensor, as an argument of the library's (None: no tensor)."""
+    return t.data_ptr() if t is not None else None
+
+
+# the current stream's address without a stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(dev: torch.device, fn: str, *args):
+    """One call on ``dev``'s current stream, with ``dev`` current."""
+    call = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        status = call(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, _raw_stream(dev.index))
+    check(fn, status)
 
 
 def route_scored(logits: torch.Tensor, top_k: int, bias=None, score: str = "sigmoid",
@@ -88,16 +118,13 @@ def route_scored(logits: torch.Tensor, top_k: int, bias=None, score: str = "sigm
     dev = logits.device
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,))
-    topk_idx = _empty((T, top_k), torch.int32, dev) if topk_idx is None else topk_idx
-    topk_w = _empty((T, top_k), torch.float32, dev) if topk_w is None else topk_w
-    _need(topk_idx, "topk_idx", torch.int32, (T, top_k))
-    _need(topk_w, "topk_w", torch.float32, (T, top_k))
-    _same_device(dev, bias=bias, topk_idx=topk_idx, topk_w=topk_w)
+        _same_device(dev, bias)
+    topk_idx = _out(topk_idx, "topk_idx", torch.int32, (T, top_k), dev)
+    topk_w = _out(topk_w, "topk_w", torch.float32, (T, top_k), dev)
     desc = RouteDesc(T, E, top_k, _one_of(_SCORES, score, "score"), num_groups, top_groups,
-                     _one_of(_RANKS, group_rank, "group_rank"), int(bool(renormalise)), scale)
-    with torch.cuda.device(dev):
-        check("moe_route_scored", lib().moe_route_scored(
-            C.byref(desc), _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_w), _stream(dev)))
+                     _one_of(_RANKS, group_rank, "group_rank"), bool(renormalise), scale)
+    _run(dev, "moe_route_scored", C.byref(desc), logits.data_ptr(), _at(bias),
+         topk_idx.data_ptr(), topk_w.data_ptr())
     return topk_idx, topk_w
 
 
@@ -112,14 +139,11 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: 
     _need(topk_idx, "topk_idx", torch.int32, (T, topk_idx.shape[-1]))
     k = topk_idx.shape[1]
     _need(grad_w, "grad_w", torch.float32, (T, k))
-    out = _empty((T, E), torch.float32, dev) if out is None else out
-    _need(out, "grad_logits", torch.float32, (T, E))
-    _same_device(dev, topk_idx=topk_idx, grad_w=grad_w, grad_logits=out)
-    desc = RouteDesc(T, E, k, _one_of(_SCORES, score, "score"), 1, 1, 0, int(bool(renormalise)),
-                     scale)
-    with torch.cuda.device(dev):
-        check("moe_route_scored_backward", lib().moe_route_scored_backward(
-            C.byref(desc), _ptr(logits), _ptr(topk_idx), _ptr(grad_w), _ptr(out), _stream(dev)))
+    _same_device(dev, topk_idx, grad_w)
+    out = _out(out, "grad_logits", torch.float32, (T, E), dev)
+    desc = RouteDesc(T, E, k, _one_of(_SCORES, score, "score"), 1, 1, 0, bool(renormalise), scale)
+    _run(dev, "moe_route_scored_backward", C.byref(desc), logits.data_ptr(), topk_idx.data_ptr(),
+         grad_w.data_ptr(), out.data_ptr())
     return out
 
 
@@ -404,27 +428,27 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none", resid
     linear_backward. ``out`` may be ``residual``. fp32 sums, one rounding."""
     dev = x.device
     M, N = x.shape[0], w.shape[0]
+    dt = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    if out_dtype is not None and dt != out_dtype:
+        raise TypeError(f"out must be {out_dtype} (got {dt})")
+    if dt != x.dtype and dt != torch.float32:
+        raise TypeError(f"out must be {x.dtype} or fp32 (got {dt})")
+    desc = _linear_desc(x, w, act, dt == torch.float32, N)
     if out is None:
-        dt = x.dtype if out_dtype is None else out_dtype
-        out = _empty((M, N), dt, dev)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out must be {out_dtype} (got {out.dtype})")
-    if out.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"out must be {x.dtype} or fp32 (got {out.dtype})")
-    desc = _linear_desc(x, w, act, out.dtype == torch.float32,
-                        _need_rows(out, "out", out.dtype, (M, N)))
+        out = torch.empty((M, N), dtype=dt, device=dev)
+    else:
+        desc.ldy = _need_rows(out, "out", dt, (M, N))
     if bias is not None:
         _need(bias, "bias", torch.float32, (N,))
     if residual is not None:
         desc.ldr = _need_rows(residual, "residual", x.dtype, (M, N))
     if pre is not None:
         desc.ldp = _need_rows(pre, "pre", x.dtype, (M, N))
-    _same_device(dev, w=w, bias=bias, residual=residual, out=out, pre=pre, workspace=workspace)
-    ws = _linear_workspace(int(lib().moe_linear_workspace_bytes(C.byref(desc))), workspace, dev)
-    with torch.cuda.device(dev):
-        check("moe_linear", lib().moe_linear(
-            C.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), _ptr(pre),
-            _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    _same_device(dev, w, bias, residual, out, pre, workspace)
+    d = C.byref(desc)
+    ws = _linear_workspace(lib().moe_linear_workspace_bytes(d), workspace, dev)
+    _run(dev, "moe_linear", d, x.data_ptr(), w.data_ptr(), _at(bias), _at(residual),
+         out.data_ptr(), _at(pre), _at(ws), 0 if ws is None else ws.numel())
     return out
 
 
@@ -447,32 +471,20 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
         desc.ldp = _need_rows(pre, "pre", x.dtype, (M, N))
     else:
         pre = None
-    if want_dx:
-        dx = _empty((M, K), x.dtype, dev) if dx is None else dx
-        _need(dx, "dx", x.dtype, (M, K))
-    else:
-        dx = None
+    dx = _out(dx, "dx", x.dtype, (M, K), dev) if want_dx else None
     if want_dw:
         if desc.w_order:
-            dw = _empty((K, N), x.dtype, dev).t() if dw is None else dw
-            _need(dw.t(), "dw.t()", x.dtype, (K, N))
+            dw = _out(None if dw is None else dw.t(), "dw.t()", x.dtype, (K, N), dev).t()
         else:
-            dw = _empty((N, K), x.dtype, dev) if dw is None else dw
-            _need(dw, "dw", x.dtype, (N, K))
+            dw = _out(dw, "dw", x.dtype, (N, K), dev)
     else:
         dw = None
-    if want_dbias:
-        dbias = _empty((N,), torch.float32, dev) if dbias is None else dbias
-        _need(dbias, "dbias", torch.float32, (N,))
-    else:
-        dbias = None
-    _same_device(dev, dy=dy, w=w, pre=pre, dx=dx, dw=dw, dbias=dbias, workspace=workspace)
-    ws = _linear_workspace(int(lib().moe_linear_backward_workspace_bytes(C.byref(desc))),
-                           workspace, dev)
-    with torch.cuda.device(dev):
-        check("moe_linear_backward", lib().moe_linear_backward(
-            C.byref(desc), _ptr(dy), _ptr(x), _ptr(w), _ptr(pre), _ptr(dx), _ptr(dw),
-            _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel(), _stream(dev)))
+    dbias = _out(dbias, "dbias", torch.float32, (N,), dev) if want_dbias else None
+    _same_device(dev, dy, w, pre, workspace)
+    d = C.byref(desc)
+    ws = _linear_workspace(lib().moe_linear_backward_workspace_bytes(d), workspace, dev)
+    _run(dev, "moe_linear_backward", d, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _at(pre),
+         _at(dx), _at(dw), _at(dbias), _at(ws), 0 if ws is None else ws.numel())
     return dx, dw, dbias
 
 
@@ -634,48 +646,50 @@ def grouped_down_wgrad(h, dy, offsets, counts, dw2=None):
 def _tensor_refs(grads, out=None):
     """(host array of moe_tensor_ref, count, device) of contiguous GPU tensors."""
     grads = list(grads)
-    out = grads if out is None else list(out)
-    if len(out) != len(grads):
-        raise ValueError(f"{len(grads)} gradients, {len(out)} outputs")
     if not grads:
         raise ValueError("no gradients")
-    dev = grads[0].device
-    words = array("q")
-    for g, o in zip(grads, out):
-        if not g.is_cuda or g.device != dev or o.device != dev:
-            raise ValueError(f"gradients and outputs must be on one GPU (got {g.device}, {o.device}, {dev})")
-        if g.dtype not in _ROWS or o.dtype != g.dtype:
-            raise TypeError(f"gradients must be bf16, fp16 or fp32, outputs alike (got {g.dtype}, {o.dtype})")
-        if not g.is_contiguous() or not o.is_contiguous():
-            raise ValueError("gradients and outputs must be contiguous")
-        if o is not g and o.shape != g.shape:
-            raise ValueError(f"output of shape {tuple(o.shape)} for a gradient of {tuple(g.shape)}")
-        # data, out, numel, then dtype and reserved in one word
-        words.extend((g.data_ptr(), o.data_ptr(), g.numel(), _ROWS[g.dtype]))
-    return words, len(grads), dev
+    n, dev = len(grads), grads[0].device
+    out = None if out is None else list(out)
+    both = grads if out is None else grads + out
+    # (list by list rather than tensor by tensor: there are many)
+    kinds = [_ROWS.get(t.dtype) for t in both]
+    if None in kinds:
+        raise TypeError(f"gradients must be bf16, fp16 or fp32 (got {both[kinds.index(None)].dtype})")
+    index = dev.index if dev.type == "cuda" else -1
+    if index < 0 or any([t.get_device() != index for t in both]):
+        raise ValueError("gradients and outputs must be on one GPU")
+    if not all([t.is_contiguous() for t in both]):
+        raise ValueError("gradients and outputs must be contiguous")
+    if out is not None:
+        if [t.shape for t in out] != [t.shape for t in grads]:
+            raise ValueError("outputs must be as many as the gradients, and of their shapes")
+        if kinds[:n] != kinds[n:]:
+            raise TypeError("outputs must have the gradients' types")
+    places = [t.data_ptr() for t in both]
+    words = array("q", bytes(32 * n))
+    # data, out, numel, then dtype and reserved in one word
+    words[0::4] = array("q", places[:n])
+    words[1::4] = array("q", places[-n:])
+    words[2::4] = array("q", [t.numel() for t in grads])
+    words[3::4] = array("q", kinds[:n])
+    return words, n, dev
 
 
 def _sumsq(words, n, dev, out):
-    refs = C.c_void_p(words.buffer_info()[0])
-    ws = _empty((int(lib().moe_grad_sumsq_workspace_bytes(refs, n)),), torch.uint8, dev)
-    out = _empty((1,), torch.float64, dev) if out is None else out
-    _need(out, "sumsq", torch.float64, (1,))
-    _same_device(dev, sumsq=out)
-    with torch.cuda.device(dev):
-        check("moe_grad_sumsq", lib().moe_grad_sumsq(refs, n, _ptr(out), _ptr(ws), ws.numel(),
-                                                     _stream(dev)))
+    refs = words.buffer_info()[0]
+    ws = torch.empty((lib().moe_grad_sumsq_workspace_bytes(refs, n),), dtype=torch.uint8,
+                     device=dev)
+    out = _out(out, "sumsq", torch.float64, (1,), dev)
+    _run(dev, "moe_grad_sumsq", refs, n, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
 def _clip(words, n, dev, sumsq, max_norm, norm):
-    norm = _empty((1,), torch.float32, dev) if norm is None else norm
     _need(sumsq, "sumsq", torch.float64, (1,))
-    _need(norm, "norm", torch.float32, (1,))
-    _same_device(dev, sumsq=sumsq, norm=norm)
-    with torch.cuda.device(dev):
-        check("moe_grad_clip", lib().moe_grad_clip(
-            C.c_void_p(words.buffer_info()[0]), n, _ptr(sumsq), max_norm, _ptr(norm),
-            _stream(dev)))
+    _same_device(dev, sumsq)
+    norm = _out(norm, "norm", torch.float32, (1,), dev)
+    _run(dev, "moe_grad_clip", words.buffer_info()[0], n, sumsq.data_ptr(), max_norm,
+         norm.data_ptr())
     return norm
 
 
