@@ -60,38 +60,74 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   const int64_t r1 = min(a.M, r0 + a.rows_per_block);
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (n < a.N) {
-    const bool full = a.vec && n + 8 <= a.N;
-    for (int64_t m = r0 + ry; m < r1; m += 8) {
-      float d[8], z[8];
-      if (full) {
-        if (a.dy_f32) {
-          const float* p = static_cast<const float*>(a.dy) + m * a.ldy + n;
-          const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
+    const int cols = min(8, a.N - n);
+    // dz of row m, its sums and its store
+    auto finish = [&](int64_t m, float (&d)[8], const float (&z)[8]) __attribute__((always_inline)) {
+      if (a.pre) {
+        switch (a.act) {  // one uniform branch for the eight
+          case MOE_ACT_RELU:
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[i] = x[i], d[4 + i] = y[i];
-        } else {
-          unpack8x16(*reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dy) + m * a.ldy + n),
-                     d, a.f16);
+            for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], MOE_ACT_RELU);
+            break;
+          case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], MOE_ACT_SILU);
+            break;
+          default:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] *= act_slope(z[i], MOE_ACT_GELU);
+            break;
         }
-        if (a.pre) unpack8x16(*reinterpret_cast<const u32x4*>(a.pre + m * a.ldp + n), z, a.f16);
-      } else {
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] = i < cols ? d[i] : 0.f;
+        sum[i] += d[i];
+      }
+      if (a.dz) *reinterpret_cast<u32x4*>(a.dz + m * a.ldz + n) = pack8x16(d, a.f16);
+    };
+    if (a.vec && cols == 8) {
+      constexpr int kRows = 2;  // rows whose loads are in flight together
+      for (int64_t m0 = r0 + ry; m0 < r1; m0 += 8 * kRows) {
+        u32x4 x[kRows], y[kRows], p[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const int64_t m = m0 + 8 * u;
+          if (m >= r1) continue;
+          const char* at = static_cast<const char*>(a.dy) + (m * a.ldy + n) * (a.dy_f32 ? 4 : 2);
+          x[u] = *reinterpret_cast<const u32x4*>(at);
+          if (a.dy_f32) y[u] = *reinterpret_cast<const u32x4*>(at + 16);
+          if (a.pre) p[u] = load8x16(a.pre + m * a.ldp + n);
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const int64_t m = m0 + 8 * u;
+          if (m >= r1) continue;
+          float d[8], z[8];
+          if (a.dy_f32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              d[i] = __uint_as_float(x[u][i]), d[4 + i] = __uint_as_float(y[u][i]);
+          } else {
+            unpack8x16(x[u], d, a.f16);
+          }
+          if (a.pre) unpack8x16(p[u], z, a.f16);
+          finish(m, d, z);
+        }
+      }
+    } else {
+      for (int64_t m = r0 + ry; m < r1; m += 8) {
+        float d[8], z[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool in = n + i < a.N;
+          const bool in = i < cols;
           d[i] = !in ? 0.f
                      : a.dy_f32 ? static_cast<const float*>(a.dy)[m * a.ldy + n + i]
                                 : from16(static_cast<const uint16_t*>(a.dy)[m * a.ldy + n + i], a.f16);
           z[i] = in && a.pre ? from16(a.pre[m * a.ldp + n + i], a.f16) : 0.f;
         }
+        finish(m, d, z);
       }
-      if (a.pre) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < a.N) d[i] *= act_slope(z[i], a.act);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[i];
-      if (a.dz) *reinterpret_cast<u32x4*>(a.dz + m * a.ldz + n) = pack8x16(d, a.f16);
     }
   }
   if (!a.sums) return;
@@ -106,14 +142,29 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   if (col < a.nw) a.sums[int64_t(blockIdx.y) * a.nw + col] = s;
 }
 
-// dbias[n] = the blocks' column sums, added in order in fp64
+// dbias[n] = the blocks' column sums, added in order in fp64: 64 columns to a
+// workgroup, each of its four wavefronts a quarter of the blocks.
 __global__ __launch_bounds__(256) void bias_grad_kernel(const float* sums, int blocks, int64_t nw,
                                                         int N, float* dbias) {
-  const int n = int(blockIdx.x) * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ double part[4][64];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int n = int(blockIdx.x) * 64 + c;
+  const int per = (blocks + 3) / 4, b0 = q * per, b1 = min(blocks, b0 + per);
   double s = 0.0;
-  for (int b = 0; b < blocks; ++b) s += double(sums[b * nw + n]);
-  dbias[n] = static_cast<float>(s);
+  if (n < N) {
+    constexpr int kBatch = 8;  // loads in flight together
+    for (int b = b0; b < b1; b += kBatch) {
+      float x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) x[u] = b + u < b1 ? sums[(b + u) * nw + n] : 0.f;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) s += double(x[u]);
+    }
+  }
+  part[q][c] = s;
+  __syncthreads();
+  if (q == 0 && n < N)
+    dbias[n] = static_cast<float>(part[0][c] + part[1][c] + part[2][c] + part[3][c]);
 }
 
 // ---- host
@@ -268,9 +319,9 @@ BackwardPlan plan_backward(const moe_linear_desc& d) {
   const int64_t M = d.rows, N = d.cols, K = d.inner;
   p.ldz = (N + 7) / 8 * 8;
   p.dz_bytes = round256(M * p.ldz * 2);
-  // about four workgroups of 256 columns to a compute unit, 8 rows at least
+  // about sixteen workgroups of 256 columns to a compute unit, 8 rows at least
   const int64_t cols = (N + 255) / 256;
-  const int64_t want = std::max<int64_t>(1, 4 * device_cu_count() / cols);
+  const int64_t want = std::max<int64_t>(1, 16 * device_cu_count() / cols);
   p.rows_per_block = static_cast<int>(std::max<int64_t>(8, ((M + want - 1) / want + 7) / 8 * 8));
   p.row_blocks = static_cast<int>((M + p.rows_per_block - 1) / p.rows_per_block);
   p.sums_bytes = round256(int64_t(p.row_blocks) * p.ldz * 4);
@@ -334,7 +385,7 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const void* dy, cons
     if (hipError_t err = hipGetLastError()) return err;
   }
   if (dbias) {
-    bias_grad_kernel<<<dim3((N + 255) / 256), 256, 0, s>>>(sums, p.row_blocks, p.ldz, N, dbias);
+    bias_grad_kernel<<<dim3((N + 63) / 64), 256, 0, s>>>(sums, p.row_blocks, p.ldz, N, dbias);
     if (hipError_t err = hipGetLastError()) return err;
   }
   const uint16_t* z = copy ? dz : static_cast<const uint16_t*>(dy);
