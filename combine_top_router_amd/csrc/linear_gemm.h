@@ -169,11 +169,12 @@ __device__ __forceinline__ void finish8(const Epilogue& e, const Block& b, int r
   }
   if (e.out_f32) {
     float* o = reinterpret_cast<float*>(b.out) + (r * b.ldo + c);
-    *reinterpret_cast<f32x4*>(o) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(o));
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4*>(o + 4));
   } else {
-    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(b.out) + (r * b.ldo + c)) =
-        pack8x16(v, e.f16);
+    __builtin_nontemporal_store(
+        pack8x16(v, e.f16),
+        reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(b.out) + (r * b.ldo + c)));
   }
 }
 
