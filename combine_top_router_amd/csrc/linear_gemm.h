@@ -92,7 +92,7 @@ __device__ __forceinline__ float normal_cdf(float z, float& g) {
 
 __device__ __forceinline__ float act_of(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : z * 0.f;  // NaN stays NaN
+    case MOE_ACT_RELU: return z != z ? z : fmaxf(z, 0.f);  // NaN stays NaN
     case MOE_ACT_SILU: return z * sigmoid(z);
     case MOE_ACT_GELU: {
       float g;

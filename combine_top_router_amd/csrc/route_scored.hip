@@ -378,7 +378,10 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
     const float l2 = __shfl_down(lj, 1, G), b2 = __shfl_down(bj, 1, G), v2 = __shfl_down(vj, 1, G),
                 off_2 = __shfl_down(off_j, 1, G);
     if (held) sure = sure && vj > -INFINITY;
-    if (mine && j + 1 < rounds) near = !(vj - v2 > off_j + off_2 || (lj == l2 && bj == b2));
+    const int e2 = __shfl_down(my_e, 1, G);
+    // (a true tie may stand in the order of the places in two lanes)
+    if (mine && j + 1 < rounds)
+      near = !(vj - v2 > off_j + off_2 || (lj == l2 && bj == b2 && my_e < e2));
     if (j + 1 == a.k && rounds == a.k + 2)
       sure = sure && vj - vb > off_j + off_b + 0x1p-16f * fabsf(vb);
   }

@@ -472,7 +472,8 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
  * A masked row's values reach that row of y alone.
  * Limits: 0 <= rows < 2^31, 8 <= inner, 1 <= cols, both <= 2^20; dtype MOE_ROWS_BF16 or
  * MOE_ROWS_F16; inner, ldx and ldw multiples of 8; MOE_W_KN: cols a multiple of 8 too
- * (else MOE_ERR_UNSUPPORTED); strides at least the row length and at most 2^21.
+ * and (rows / 128 + 1) * (max(inner, cols) / 32 + 1) <= 2^22 (else
+ * MOE_ERR_UNSUPPORTED); strides at least the row length and at most 2^21.
  *   workspace_d >= moe_linear_workspace_bytes(desc) bytes, 16-byte aligned (NULL if that
  *   is 0); contents on entry do not matter. Calls that may overlap need workspaces of their own.
  */

@@ -22,7 +22,7 @@ def _phi(z):
 
 def act(z, name: str):
     if name == "relu":
-        return np.where(z > 0, z, z * 0.0)
+        return np.where(z > 0, z, np.where(np.isnan(z), z, 0.0))
     if name == "silu":
         with np.errstate(over="ignore"):
             return z / (1.0 + np.exp(-z))

@@ -142,6 +142,22 @@ def test_close_scores_are_told_apart_as_in_64_bits():
                 _check(logits, 8, b, score, groups, top, "max", True, 1.0)
 
 
+@pytest.mark.parametrize("T,E,k,groups,top", [(40, 256, 8, 1, 1), (2100, 256, 8, 8, 4),
+                                              (17000, 128, 7, 1, 1), (17000, 256, 8, 8, 4),
+                                              (4200, 500, 16, 4, 2), (9000, 60, 4, 6, 2)])
+def test_ties_between_experts_of_different_lanes(T, E, k, groups, top):
+    """Logits on a coarse grid: most tokens have ties among the chosen and at the border."""
+    print("CASE ties", T, E, k, groups, top, flush=True)
+    gen = torch.Generator("cuda").manual_seed(T + E)
+    logits = torch.round(torch.randn((T, E), generator=gen, device="cuda") * 4) / 4
+    bias = torch.round(torch.randn((E,), generator=gen, device="cuda") * 2) / 8
+    for score in ("sigmoid", "softmax"):
+        # one expert's value decides a group's rank: sums of two different pairs that agree
+        # but for fp64's own rounding are no ties
+        for b in (None, bias):
+            _check(logits, k, b if score == "sigmoid" else None, score, groups, top, "max", True, 1.0)
+
+
 def test_repeated_and_foreign_ids_in_the_backward():
     logits = torch.randn((5, 20), generator=torch.Generator("cuda").manual_seed(4), device="cuda")
     idx = torch.tensor([[3, 3, 3, 1], [-1, 20, 4, 4], [-5, -1, 99, 20], [0, 19, 0, 19],
