@@ -351,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
   // The candidates' values again, each from its own logit, against the next one's:
   // far enough apart (or a true tie), or `near`. The keys order values of which they leave
   // out the last bits, at most 2^-17 of a value: `beyond`, and all that was not
-  // looked at, has to lie that much below the k-th.
+  // looked at, has to lie that much (of both) below the k-th.
   const bool mine = j < a.k, held = j < min(rounds, a.k + 1);
   bool near = false;
   const float lj = clean(row[my_e]);
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
     if (mine && j + 1 < rounds)
       near = !(vj - v2 > off_j + off_2 || (lj == l2 && bj == b2 && my_e < e2));
     if (j + 1 == a.k && rounds == a.k + 2)
-      sure = sure && vj - vb > off_j + off_b + 0x1p-16f * fabsf(vb);
+      sure = sure && vj - vb > off_j + off_b + 0x1.8p-17f * (fabsf(vj) + fabsf(vb));
   }
   float ls = lj;
   if (__any(!sure) || (!a.sigmoid && a.bias && __any(near))) {
