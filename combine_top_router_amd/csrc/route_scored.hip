@@ -417,9 +417,10 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
     ls = clean(row[my_e]);
   } else if (__any(near)) {
     // the candidates are the right ones, their order is that of their fp64 values
-    // (softmax: without its common factor)
-    const double v = a.sigmoid ? 1.0 / (1.0 + exp(-double(lj))) + double(bj)
-                               : exp(double(lj) - double(lmax));
+    // (softmax: without its common factor; 0 at -inf, also where lmax is -inf itself)
+    const double v = a.sigmoid         ? 1.0 / (1.0 + exp(-double(lj))) + double(bj)
+                     : lj == -INFINITY ? 0.0
+                                       : exp(double(lj) - double(lmax));
     int place = 0;
     for (int i = 0; i < min(rounds, a.k + 1); ++i) {
       const double vi = __shfl(v, i, G);

@@ -241,3 +241,17 @@ def test_captured_call_replays_on_new_logits():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (idx, w, grad)))
+
+
+@pytest.mark.parametrize("E,k", [(8, 7), (8, 8), (9, 8), (16, 15), (16, 16), (32, 16)])
+@pytest.mark.parametrize("T", [3, 2100])
+def test_empty_rows_where_nearly_every_expert_is_chosen(T, E, k):
+    """Rows of -inf or NaN alone, with no expert left over or one: all scores are
+    0, so the lowest ids in order, also beside rows that are not empty."""
+    print("CASE empty rows", T, E, k, flush=True)
+    logits = torch.randn((T, E), generator=torch.Generator("cuda").manual_seed(E), device="cuda")
+    logits[0::3] = float("-inf")
+    logits[1::6] = float("nan")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            _check(logits, k, None, score, 1, 1, "max", renorm, 1.0)
