@@ -341,7 +341,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
     const float highest = group_max<G>(in && !keep ? rank : -INFINITY);
     // (softmax: no score is above 1 / sum; not greater: infinities too are left to
     // the exact choice)
-    const float off = a.sigmoid ? 0x1p-19f : a.bias ? 0x1p-15f * inv : 0x1p-16f * lowest;
+    const float off = a.sigmoid ? 0x1p-19f : (a.bias ? 0x1p-15f * inv : 0x1p-16f * lowest) + 0x1p-126f;
     sure = lowest - highest > off + 0x1p-21f * (fabsf(lowest) + fabsf(highest));
   }
 
@@ -391,7 +391,9 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
       } else {
         far = lmax - l;
         x = (l == -INFINITY ? 0.f : expf(-far)) * inv;
-        off = x > 0.f ? x * ((a.bias ? 64.f : 8.f) + far) * 0x1p-24f : 0.f;
+        // (below the normal range the roundings, and the bits that a key leaves out, are whole
+        // smallest steps, 2^-143 at most; a score that is 0 by its formula is exact)
+        off = l > -INFINITY ? x * ((a.bias ? 64.f : 8.f) + far) * 0x1p-24f + 0x1p-126f : 0.f;
       }
       const float v = fmaxf(x + bias, -INFINITY);
       off += 0x1p-23f * fabsf(v);

@@ -255,3 +255,15 @@ def test_empty_rows_where_nearly_every_expert_is_chosen(T, E, k):
     for score in ("softmax", "sigmoid"):
         for renorm in (True, False):
             _check(logits, k, None, score, 1, 1, "max", renorm, 1.0)
+
+
+@pytest.mark.parametrize("groups,top", [(1, 1), (8, 3)])
+def test_scores_below_the_normal_range_are_told_apart_as_in_64_bits(groups, top):
+    """Softmax scores of a few smallest steps of fp32, far below the first expert's."""
+    print("CASE tiny scores", groups, top, flush=True)
+    gen = torch.Generator("cuda").manual_seed(11)
+    logits = -98.0 - 5.5 * torch.rand((2100, 64), generator=gen, device="cuda")
+    logits[:, 5] = 0.0
+    for renorm in (True, False):
+        _check(logits, 8, None, "softmax", groups, top, "max", renorm, 1.0)
+    _check(logits, 8, torch.zeros(64, device="cuda"), "softmax", groups, top, "max", True, 1.0)
