@@ -54,7 +54,11 @@ class MoELayer:
         """w1, w3: [E_loc, H, I] and w2: [E_loc, I, H], bf16 on the GPU (math
         orientation); repacked once here into the GEMM's layout. gate_w: the
         router projection [E, H] bf16 (then no logits are given to the layer).
-        shared: a shared expert's (w1, w3 [H, Is], w2 [Is, H]) bf16, contiguous."""
+        shared: a shared expert's (w1, w3 [H, Is], w2 [Is, H]) bf16, contiguous; not
+        for one rank's share of the experts, whose output the ranks add up."""
+        if shared is not None and ep_size > 1 and local_rank >= 0:
+            raise ValueError("a rank's share of the experts takes no shared expert: the sum over "
+                             "the ranks would count it on each of them")
         dev = w1.device
         self.T, self.H, self.E, self.k, self.I = num_tokens, hidden, num_experts, top_k, inter
         self.desc = ops.layout_desc(num_tokens, num_experts, top_k, ep_size, local_rank, align)

@@ -111,3 +111,11 @@ def test_workspace_does_not_depend_on_strides_or_types():
         a = call(C.byref(_desc(inner=8192, ldx=8192, ldw=8192)))
         b = call(C.byref(_desc(inner=8192, ldx=9000, ldw=8200, ldy=64, act=3, dtype=1, y_f32=1)))
         assert a == b > 0
+
+
+def test_a_rank_share_takes_no_shared_expert():
+    torch = pytest.importorskip("torch")
+    from combine_top_router_amd import MoELayer
+    w = torch.zeros((4, 128, 128), dtype=torch.bfloat16)  # refused before anything is on a GPU
+    with pytest.raises(ValueError, match="shared expert"):
+        MoELayer(16, 128, 8, 2, 128, w, w, w, ep_size=2, local_rank=1, shared=(w[0], w[0], w[0]))
