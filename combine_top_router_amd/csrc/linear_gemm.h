@@ -102,7 +102,10 @@ __device__ __forceinline__ float act_of(float z, int act) {
   }
 }
 
+// (an infinite z, as fp16 stores what is past its range: clamped where the slopes
+// are 0 and 1 already, or z times a vanishing factor would be NaN; NaN stays NaN)
 __device__ __forceinline__ float act_slope(float z, int act) {
+  z = z != z ? z : fminf(fmaxf(z, -1e4f), 1e4f);
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case MOE_ACT_SILU: {

@@ -505,7 +505,8 @@ int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d
  *
  *   dz = dy act'(pre)   fp32, then rounded to dtype for the two products (the
  *                       matrix cores read 16-bit values; this is the size of
- *                       the rounding the outputs have themselves)
+ *                       the rounding the outputs have themselves); act' of an
+ *                       infinite pre (z past fp16's range) is its limit
  *   dx = dz w           [rows, inner] of dtype, dense
  *   dw = dz^T x         in w's order, of dtype, dense
  *   dbias = column sums of the unrounded dz, [cols] float

@@ -32,6 +32,7 @@ def act(z, name: str):
 
 
 def act_slope(z, name: str):
+    z = np.clip(z, -1e4, 1e4)  # the slopes are 0 and 1 there: an infinite z has its limit
     if name == "relu":
         return (z > 0).astype(np.float64)
     if name == "silu":

@@ -339,3 +339,30 @@ def test_two_graphs_replay_between_eager_calls():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_slopes_of_pre_activations_past_fp16(act, f32):
+    """z outside fp16's range is stored as +-inf: its slope is 1 or 0, not NaN, and
+    that of a NaN stays one (relu: z > 0 is false)."""
+    inf, M, N, K = float("inf"), 9, 24, 16
+    gen = torch.Generator("cuda").manual_seed(8)
+    dy = torch.randn((M, N), generator=gen, device="cuda").to(torch.float32 if f32 else FP)
+    x, w = _matrix(gen, M, K, FP), _matrix(gen, N, K, FP)
+    z = torch.tensor([-inf, inf, -65504.0, 65504.0, -12.0, 12.0, -0.0, 1.0],
+                     device="cuda").repeat(M, 3).to(FP)
+    dx, dw, db = ops.linear_backward(dy, x, w, act, z, want_dbias=True)
+    # and what the same finite slopes give
+    z2 = z.clamp(-30000, 30000)
+    dx2, dw2, db2 = ops.linear_backward(dy, x, w, act, z2, want_dbias=True)
+    torch.cuda.synchronize()
+    assert torch.isfinite(db).all()
+    for a, b in ((dx, dx2), (dw, dw2), (db, db2)):
+        assert torch.equal(a, b)
+    assert not db[0::8].any() and torch.equal(db[1::8], ops.linear_backward(
+        dy, x, w, want_dx=False, want_dw=False, want_dbias=True)[2][1::8])
+    z[3, 5] = float("nan")
+    db = ops.linear_backward(dy, x, w, act, z, False, False, True)[2]
+    torch.cuda.synchronize()
+    assert torch.isnan(db).nonzero().flatten().tolist() == ([] if act == "relu" else [5])
