@@ -69,6 +69,12 @@ def _one_of(table: dict, key, name: str) -> int:
     return table[key]
 
 
+def _int32(*sizes):
+    """Refuses what a descriptor's 32-bit field would cut short."""
+    if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:
+        raise ValueError(f"sizes must fit 32 bits (got {sizes})")
+
+
 def _same_device(dev: torch.device, *tensors):
     for t in tensors:
         if t is not None and t.device != dev:
@@ -116,6 +122,7 @@ def route_scored(logits: torch.Tensor, top_k: int, bias=None, score: str = "sigm
     _need(logits, "logits", torch.float32)
     T, E = logits.shape
     dev = logits.device
+    _int32(E, top_k, num_groups, top_groups)
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,))
         _same_device(dev, bias)
@@ -138,6 +145,7 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_w: 
     dev = logits.device
     _need(topk_idx, "topk_idx", torch.int32, (T, topk_idx.shape[-1]))
     k = topk_idx.shape[1]
+    _int32(E, k)
     _need(grad_w, "grad_w", torch.float32, (T, k))
     _same_device(dev, topk_idx, grad_w)
     out = _out(out, "grad_logits", torch.float32, (T, E), dev)
@@ -388,6 +396,7 @@ def _linear_desc(x, w, act, y_f32, ldy):
         raise TypeError(f"x must be bf16 or fp16 (got {x.dtype})")
     M, K = x.shape
     N = w.shape[0]
+    _int32(K, N)
     ldx = _need_rows(x, "x", x.dtype, (M, K))
     kn = w.stride(1) != 1 and w.stride(0) == 1  # a transposed [inner, cols] matrix
     ldw = _need_rows(w.t(), "w.t()", x.dtype, (K, N)) if kn else _need_rows(w, "w", x.dtype, (N, K))

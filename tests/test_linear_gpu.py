@@ -366,3 +366,9 @@ def test_slopes_of_pre_activations_past_fp16(act, f32):
     db = ops.linear_backward(dy, x, w, act, z, False, False, True)[2]
     torch.cuda.synchronize()
     assert torch.isnan(db).nonzero().flatten().tolist() == ([] if act == "relu" else [5])
+
+
+def test_sizes_past_32_bits_are_refused():
+    x = torch.empty((1, 2 ** 32 + 8), dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        ops.linear(x, x)

@@ -267,3 +267,11 @@ def test_scores_below_the_normal_range_are_told_apart_as_in_64_bits(groups, top)
     for renorm in (True, False):
         _check(logits, 8, None, "softmax", groups, top, "max", renorm, 1.0)
     _check(logits, 8, torch.zeros(64, device="cuda"), "softmax", groups, top, "max", True, 1.0)
+
+
+def test_arguments_past_32_bits_are_refused():
+    x = torch.zeros((4, 32), device="cuda")
+    for bad in (dict(top_k=2 ** 32 + 4), dict(num_groups=2 ** 32 + 1),
+                dict(num_groups=1 - 2 ** 32), dict(top_groups=2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            ops.route_scored(x, **{"top_k": 4, **bad})
