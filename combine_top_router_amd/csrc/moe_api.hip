@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -526,6 +527,11 @@ static bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && aligned16(ws) && have >= need);
 }
 
+// an output that begins where a buffer does that other workgroups still read
+static bool clashes(const void* out, std::initializer_list<const void*> read) {
+  return out && std::find(read.begin(), read.end(), out) != read.end();
+}
+
 int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d,
                    const float* bias_d, const void* residual_d, void* y_d, void* pre_d,
                    void* workspace_d, size_t workspace_bytes, void* stream) {
@@ -535,7 +541,8 @@ int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d
   if ((residual_d && !row_stride_ok(desc->ldr, desc->cols)) ||
       (pre_d && !row_stride_ok(desc->ldp, desc->cols)))
     return MOE_ERR_ARG;
-  if (pre_d && (pre_d == y_d || pre_d == residual_d)) return MOE_ERR_ARG;
+  if (clashes(y_d, {x_d, w_d, bias_d}) || clashes(pre_d, {x_d, w_d, bias_d, residual_d, y_d}))
+    return MOE_ERR_ARG;
   if (residual_d == y_d && (desc->y_f32 || desc->ldr != desc->ldy)) return MOE_ERR_ARG;
   if (!workspace_ok(workspace_d, workspace_bytes, moe::linear_workspace_bytes(*desc)))
     return MOE_ERR_ARG;
@@ -557,6 +564,9 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
     if (dw_d && (!x_d || !aligned16(x_d))) return MOE_ERR_ARG;
   }
   if (!aligned16(dx_d) || !aligned16(dw_d)) return MOE_ERR_ARG;
+  if (clashes(dx_d, {dy_d, x_d, w_d, pre_d}) || clashes(dw_d, {dy_d, x_d, w_d, pre_d, dx_d}) ||
+      clashes(dbias_d, {dy_d, x_d, w_d, pre_d, dx_d, dw_d}))
+    return MOE_ERR_ARG;
   if (!workspace_ok(workspace_d, workspace_bytes, moe::linear_backward_workspace_bytes(*desc)))
     return MOE_ERR_ARG;
   return status_of(moe::launch_linear_backward(*desc, dy_d, x_d, w_d, pre_d, dx_d, dw_d, dbias_d,

@@ -434,7 +434,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none", resid
     """act(x w^T + bias) + residual: x [M, K], w [N, K] bf16 or fp16 (w contiguous, or
     the transpose of a contiguous [K, N] matrix), bias [N] fp32, residual [M, N]
     as x; the result as x or fp32. ``pre``, if given, receives x w^T + bias for
-    linear_backward. ``out`` may be ``residual``. fp32 sums, one rounding."""
+    linear_backward. ``out`` may be ``residual``; no other output may share memory
+    with a tensor of the call. fp32 sums, one rounding."""
     dev = x.device
     M, N = x.shape[0], w.shape[0]
     dt = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
@@ -466,7 +467,8 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
                     want_dbias: bool = False, dx=None, dw=None, dbias=None, workspace=None):
     """(dx [M, K], dw [N, K], dbias [N] fp32) from dy [M, N] (as x, or fp32), None
     for those not wanted. ``pre`` is linear's pre-activation (for act other than
-    "none"); dw lies in memory as w does. The residual's gradient is dy."""
+    "none"); dw lies in memory as w does. The residual's gradient is dy. No output
+    may share memory with a tensor of the call."""
     dev = x.device
     M, K = x.shape
     N = w.shape[0]

@@ -468,7 +468,7 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
  *   y_d         [rows, cols] of `dtype` or (y_f32) float, row stride ldy (out)
  *   pre_d       [rows, cols] of `dtype`, row stride ldp, or NULL (out)
  * y may be the residual itself (same address, stride and type); other buffers
- * must not overlap. Strides are in elements; ldr and ldp are read only where their buffer is given.
+ * must not overlap (an output that begins where another buffer does is refused). Strides are in elements; ldr and ldp are read only where their buffer is given.
  * A masked row's values reach that row of y alone.
  * Limits: 0 <= rows < 2^31, 8 <= inner, 1 <= cols, both <= 2^20; dtype MOE_ROWS_BF16 or
  * MOE_ROWS_F16; inner, ldx and ldw multiples of 8; MOE_W_KN: cols a multiple of 8 too

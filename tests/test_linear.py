@@ -119,3 +119,28 @@ def test_a_rank_share_takes_no_shared_expert():
     w = torch.zeros((4, 128, 128), dtype=torch.bfloat16)  # refused before anything is on a GPU
     with pytest.raises(ValueError, match="shared expert"):
         MoELayer(16, 128, 8, 2, 128, w, w, w, ep_size=2, local_rank=1, shared=(w[0], w[0], w[0]))
+
+
+@built
+def test_outputs_in_an_operand_are_refused():
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    d = _desc()
+    at = [C.c_void_p((i + 1) << 20) for i in range(8)]  # never dereferenced
+    ws = C.c_void_p(1 << 30)
+
+    def forward(x, w, bias, res, y, pre):
+        return lib.moe_linear(C.byref(d), x, w, bias, res, y, pre, ws, 1 << 40, None)
+
+    def backward(dy, x, w, pre, dx, dw, db):
+        return lib.moe_linear_backward(C.byref(d), dy, x, w, pre, dx, dw, db, ws, 1 << 40, None)
+    for out, operands in ((4, (0, 1, 2)), (5, (0, 1, 2, 3, 4))):
+        for i in operands:
+            args = at[:6]
+            args[out] = args[i]
+            assert forward(*args) == 1
+    for out, operands in ((4, (0, 1, 2, 3)), (5, (0, 1, 2, 3, 4)), (6, (0, 1, 2, 3, 4, 5))):
+        for i in operands:
+            args = at[:7]
+            args[out] = args[i]
+            assert backward(*args) == 1
