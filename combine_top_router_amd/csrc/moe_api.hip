@@ -113,7 +113,8 @@ static int32_t route_desc_status(const moe_route_desc* d) {
     return MOE_ERR_ARG;
   if (d->renormalise != 0 && d->renormalise != 1) return MOE_ERR_ARG;
   if (!std::isfinite(d->scale)) return MOE_ERR_ARG;
-  if (d->num_tokens > (int64_t(1) << 31) / d->top_k) return MOE_ERR_ARG;
+  // a launch has up to 64 lanes a token, and fewer than 2^32 of them
+  if (d->num_tokens >= int64_t(1) << 26) return MOE_ERR_ARG;
   return MOE_OK;
 }
 

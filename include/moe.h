@@ -101,7 +101,7 @@ int32_t moe_route(const float* logits_d, int64_t num_tokens, int32_t num_experts
  *   logits_d    [T, E] float
  *   bias_d      [E] float, or NULL
  *   topk_idx_d  [T, k] int32 (out);  topk_w_d [T, k] float (out)
- * Limits: T >= 0, 1 <= E <= 1024, 1 <= num_groups <= 64 dividing E,
+ * Limits: 0 <= T < 2^26, 1 <= E <= 1024, 1 <= num_groups <= 64 dividing E,
  * 1 <= top_groups <= num_groups, 1 <= k <= min(16, top_groups * E / num_groups),
  * finite scale. T = 0 is a no-op.
  */

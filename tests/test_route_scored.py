@@ -106,3 +106,13 @@ def test_null_pointers_and_empty_batches():
     d.num_tokens = 0
     assert lib.moe_route_scored(C.byref(d), None, None, None, None, None) == 0
     assert lib.moe_route_scored_backward(C.byref(d), None, None, None, None, None) == 0
+
+
+@pytest.mark.skipif(not os.path.exists(LIB), reason="libmoe.so not built")
+def test_more_tokens_than_a_launch_has_lanes_for_are_refused():
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    d = _lib.RouteDesc(1 << 26, 8, 1, 1, 1, 1, 1, 1, 1.0)
+    fake = C.c_void_p(1 << 20)  # never dereferenced
+    assert lib.moe_route_scored(C.byref(d), fake, fake, fake, fake, None) == 1
+    assert lib.moe_route_scored_backward(C.byref(d), fake, fake, fake, fake, None) == 1
