@@ -72,9 +72,12 @@ __device__ __forceinline__ i32x4 make_rsrc(const void* base, uint32_t bytes) {
 // inline assembly so that the compiler does not wait for these transfers
 // before unrelated LDS reads; the kernel waits for them itself (s_waitcnt
 // vmcnt + barrier) before reading the stage they fill. The instruction has
-// no register result.
+// no register result. The compiler keeps no wait states for an instruction that
+// it does not see: the one that has to lie between a scalar write of M0 and
+// the load that reads it stands in the same block (without it the two were
+// neighbours at most places, and a load may take the M0 before).
 __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t byte_off, uint32_t lds_addr) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(byte_off), "s"(rsrc),
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(byte_off), "s"(rsrc),
                "{m0}"(lds_addr)
                : "memory");
 }
@@ -88,7 +91,7 @@ __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t byte_off, uint32_t ld
 // the same range (rows past the range are decided by voff alone).
 __device__ __forceinline__ void dma16(i32x4 rsrc, uint32_t voff, uint32_t soff,
                                       uint32_t lds_addr) {
-  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
                "{m0}"(lds_addr)
                : "memory");
 }
