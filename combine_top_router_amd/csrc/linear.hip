@@ -11,6 +11,12 @@
 // The forward reads x by rows and w by rows ([N, K]) or by columns ([K, N]);
 // dx reads dz by rows and w the other way round; dw reads both by columns.
 //
+//  * dz is an fp32 value (dy act' or an fp32 dy), and the matrix cores read
+//    16-bit ones: it goes in as two, dz = hi + lo with hi = dz rounded and lo
+//    the rest rounded (2^-16 of dz left out in bf16, 2^-22 in fp16), whose
+//    products are summed together. One 16-bit part alone, at the caller's wish,
+//    gives dx and dw a second rounding (2.4e-3 of their norm instead of 1.7e-3
+//    in bf16) and halves the products.
 //  * v_mfma_f32_32x32x16: a lane feeds 8 consecutive k of one row of A and of
 //    B. By-rows tiles give them as one 16-byte LDS read; by-columns tiles lie
 //    in LDS as in memory and are transposed on the way out
@@ -39,8 +45,8 @@
 namespace moe {
 namespace {
 
-// dz = dy act'(pre), rounded to the rows' type with its rows padded to ldz (zeros
-// past N), and the column sums of the unrounded dz over this block's rows.
+// dz = dy act'(pre), in one or two parts of the rows' type, each padded to nw
+// columns (zeros past N), and the column sums of the unrounded dz over this block's rows.
 // A thread owns eight columns; a block 8 row lanes x 32 column groups.
 struct ActGradArgs {
   const void* dy;
@@ -48,6 +54,7 @@ struct ActGradArgs {
   uint16_t* dz;         // or nullptr
   float* sums;          // [gridDim.y, nw] or nullptr
   int64_t ldy, ldp, ldz, nw, M;
+  int part;             // columns from dz's first part to its second, or 0: one part
   int N, act, rows_per_block;
   bool f16, dy_f32, vec;  // vec: rows of dy and pre start 16-byte aligned
 };
@@ -84,7 +91,16 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
         d[i] = i < cols ? d[i] : 0.f;
         sum[i] += d[i];
       }
-      if (a.dz) *reinterpret_cast<u32x4*>(a.dz + m * a.ldz + n) = pack8x16(d, a.f16);
+      if (!a.dz) return;
+      const u32x4 hi = pack8x16(d, a.f16);
+      *reinterpret_cast<u32x4*>(a.dz + m * a.ldz + n) = hi;
+      if (!a.part) return;
+      float h[8];
+      unpack8x16(hi, h, a.f16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)  // (nothing beside an infinite part: inf - inf is NaN)
+        h[i] = fabsf(h[i]) == INFINITY ? 0.f : d[i] - h[i];
+      *reinterpret_cast<u32x4*>(a.dz + m * a.ldz + a.part + n) = pack8x16(h, a.f16);
     };
     if (a.vec && cols == 8) {
       constexpr int kRows = 2;  // rows whose loads are in flight together
@@ -251,7 +267,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K) {
     int64_t M, N, K, cus;
     Plan p;
   };
-  constexpr int kKnown = 8;
+  constexpr int kKnown = 16;
   thread_local Known known[kKnown] = {};
   thread_local int next = 0;
   const int64_t cus = device_cu_count();
@@ -276,9 +292,12 @@ void launch_product(const GemmArgs& g, int tile, hipStream_t s) {
   }
 }
 
+// The reduction of a product with an operand in two parts.
+int64_t two_parts(int64_t K) { return 2 * ((K + BK - 1) / BK * BK); }
+
 hipError_t product(GemmArgs g, bool a_cols, bool b_cols, void* ws, hipStream_t s) {
   if (g.M == 0 || g.N == 0) return hipSuccess;
-  const Plan p = plan_product(g.M, g.N, g.K);
+  const Plan p = plan_product(g.M, g.N, g.two ? two_parts(g.K) : g.K);
   const Tile& c = kTiles[p.tile];
   g.tiles_m = static_cast<int>((g.M + c.bm - 1) / c.bm);
   g.tiles_n = static_cast<int>((g.N + c.bn - 1) / c.bn);
@@ -304,30 +323,33 @@ bool aligned(const void* p, int64_t ld_bytes) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld_bytes & 15) == 0);
 }
 
+int act_kind(const moe_linear_desc& d) { return d.act & ~MOE_DZ_16BIT; }
+
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // the backward's own buffers, in order: dz, the blocks' column sums, the splits' sums
 struct BackwardPlan {
-  bool copy;  // dz is written (else dy serves as it is)
-  int64_t ldz, dz_bytes, sums_bytes, part_bytes;
+  int64_t nw, dz_bytes, sums_bytes, part_bytes;
   int row_blocks, rows_per_block;
 };
 
-// The workspace has to be known before the buffers are, so it always has room for dz.
+// The workspace has to be known before the buffers are, so it always has room for
+// dz in two parts and for the splits of either product.
 BackwardPlan plan_backward(const moe_linear_desc& d) {
   BackwardPlan p{};
   const int64_t M = d.rows, N = d.cols, K = d.inner;
-  p.ldz = (N + 7) / 8 * 8;
-  p.dz_bytes = round256(M * p.ldz * 2);
+  p.nw = (N + 7) / 8 * 8;
+  p.dz_bytes = round256(M * 2 * p.nw * 2);
   // about sixteen workgroups of 256 columns to a compute unit, 8 rows at least
   const int64_t cols = (N + 255) / 256;
   const int64_t want = std::max<int64_t>(1, 16 * device_cu_count() / cols);
   p.rows_per_block = static_cast<int>(std::max<int64_t>(8, ((M + want - 1) / want + 7) / 8 * 8));
   p.row_blocks = static_cast<int>((M + p.rows_per_block - 1) / p.rows_per_block);
-  p.sums_bytes = round256(int64_t(p.row_blocks) * p.ldz * 4);
+  p.sums_bytes = round256(int64_t(p.row_blocks) * p.nw * 4);
   const bool nk = d.w_order == MOE_W_NK;
-  p.part_bytes = std::max(plan_product(M, K, N).part_bytes,
-                          (nk ? plan_product(N, K, M) : plan_product(K, N, M)).part_bytes);
+  const int64_t a = nk ? N : K, b = nk ? K : N;  // dw's rows and columns
+  p.part_bytes = std::max({plan_product(M, K, N).part_bytes, plan_product(M, K, two_parts(N)).part_bytes,
+                           plan_product(a, b, M).part_bytes, plan_product(a, b, two_parts(M)).part_bytes});
   return p;
 }
 
@@ -354,7 +376,7 @@ hipError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w,
   g.e.out = y, g.e.bias = bias;
   g.e.res = static_cast<const uint16_t*>(residual), g.e.pre = static_cast<uint16_t*>(pre);
   g.e.ldo = d.ldy, g.e.ldr = d.ldr, g.e.ldp = d.ldp;
-  g.e.act = d.act, g.e.f16 = d.dtype == MOE_ROWS_F16, g.e.out_f32 = d.y_f32 != 0;
+  g.e.act = act_kind(d), g.e.f16 = d.dtype == MOE_ROWS_F16, g.e.out_f32 = d.y_f32 != 0;
   g.e.vec = aligned(y, d.ldy * (d.y_f32 ? 4 : 2)) && aligned(residual, d.ldr * 2) &&
             aligned(pre, d.ldp * 2);
   return product(g, false, !nk, ws, s);
@@ -370,31 +392,36 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const void* dy, cons
   void* part = at + p.dz_bytes + p.sums_bytes;
   const int64_t M = d.rows;
   const int N = d.cols, K = d.inner;
-  const bool f16 = d.dtype == MOE_ROWS_F16, act = d.act != MOE_ACT_NONE, nk = d.w_order == MOE_W_NK;
+  const int act = act_kind(d);
+  const bool f16 = d.dtype == MOE_ROWS_F16, nk = d.w_order == MOE_W_NK;
   // dy is dz itself where nothing is to be done to it and its rows can be loaded as they are
-  const bool copy = (dx || dw) && (act || d.y_f32 || N % 8 || !aligned(dy, d.ldy * 2));
+  const bool copy = (dx || dw) && (act != MOE_ACT_NONE || d.y_f32 || N % 8 || !aligned(dy, d.ldy * 2));
+  // one part holds a 16-bit dy, and what relu leaves of it
+  const bool two = copy && !(d.act & MOE_DZ_16BIT) &&
+                   (d.y_f32 || act == MOE_ACT_SILU || act == MOE_ACT_GELU);
+  const int lo = two ? static_cast<int>(p.nw) : 0;  // where dz's second part begins
+  const int64_t ldz = copy ? p.nw + lo : d.ldy;
   if (M > 0 && (copy || dbias)) {
     ActGradArgs a{};
-    a.dy = dy, a.pre = act ? static_cast<const uint16_t*>(pre) : nullptr;
+    a.dy = dy, a.pre = act != MOE_ACT_NONE ? static_cast<const uint16_t*>(pre) : nullptr;
     a.dz = copy ? dz : nullptr, a.sums = dbias ? sums : nullptr;
-    a.ldy = d.ldy, a.ldp = d.ldp, a.ldz = p.ldz, a.nw = p.ldz, a.M = M;
-    a.N = N, a.act = d.act, a.rows_per_block = p.rows_per_block;
+    a.ldy = d.ldy, a.ldp = d.ldp, a.ldz = ldz, a.nw = p.nw, a.M = M;
+    a.part = lo, a.N = N, a.act = act, a.rows_per_block = p.rows_per_block;
     a.f16 = f16, a.dy_f32 = d.y_f32 != 0;
     a.vec = aligned(dy, d.ldy * (d.y_f32 ? 4 : 2)) && aligned(a.pre, d.ldp * 2);
     act_grad_kernel<<<dim3((N + 255) / 256, p.row_blocks), 256, 0, s>>>(a);
     if (hipError_t err = hipGetLastError()) return err;
   }
   if (dbias) {
-    bias_grad_kernel<<<dim3((N + 63) / 64), 256, 0, s>>>(sums, p.row_blocks, p.ldz, N, dbias);
+    bias_grad_kernel<<<dim3((N + 63) / 64), 256, 0, s>>>(sums, p.row_blocks, p.nw, N, dbias);
     if (hipError_t err = hipGetLastError()) return err;
   }
   const uint16_t* z = copy ? dz : static_cast<const uint16_t*>(dy);
-  const int64_t ldz = copy ? p.ldz : d.ldy;
-  const int z_ext = static_cast<int>(p.ldz);  // N, or N with its zeros
+  const int z_ext = static_cast<int>(p.nw);  // N, or N with its zeros
   GemmArgs g{};
-  g.e.f16 = f16, g.e.act = MOE_ACT_NONE;
+  g.e.f16 = f16, g.e.act = MOE_ACT_NONE, g.two = two ? 1 : 0;
   if (dx) {  // dx[m, k] = sum_n dz[m, n] w[n, k]
-    g.a = z, g.lda = ldz, g.a_ext = z_ext;
+    g.a = z, g.lda = ldz, g.a_ext = z_ext, g.a_part = lo;
     g.b = static_cast<const uint16_t*>(w), g.ldb = d.ldw, g.b_ext = nk ? K : N;
     g.M = M, g.N = K, g.K = N;
     g.e.out = dx, g.e.ldo = K;
@@ -405,11 +432,11 @@ hipError_t launch_linear_backward(const moe_linear_desc& d, const void* dy, cons
     const uint16_t* xs = static_cast<const uint16_t*>(x);
     g.K = M;
     if (nk) {  // dw[n, k] = sum_m dz[m, n] x[m, k]
-      g.a = z, g.lda = ldz, g.a_ext = z_ext, g.M = N;
-      g.b = xs, g.ldb = d.ldx, g.b_ext = K, g.N = K;
+      g.a = z, g.lda = ldz, g.a_ext = z_ext, g.a_part = lo, g.M = N;
+      g.b = xs, g.ldb = d.ldx, g.b_ext = K, g.b_part = 0, g.N = K;
     } else {   // dw[k, n] = sum_m x[m, k] dz[m, n]
-      g.a = xs, g.lda = d.ldx, g.a_ext = K, g.M = K;
-      g.b = z, g.ldb = ldz, g.b_ext = z_ext, g.N = N;
+      g.a = xs, g.lda = d.ldx, g.a_ext = K, g.a_part = 0, g.M = K;
+      g.b = z, g.ldb = ldz, g.b_ext = z_ext, g.b_part = lo, g.N = N;
     }
     g.e.out = dw, g.e.ldo = g.N;
     g.e.vec = aligned(dw, g.N * 2);

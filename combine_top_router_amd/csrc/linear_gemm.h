@@ -35,6 +35,8 @@ struct GemmArgs {
   int64_t lda, ldb;     // elements
   int64_t M, N, K;      // output rows and columns, reduction
   int a_ext, b_ext;     // contiguous extent of an operand's rows (reduction or output index)
+  int two;              // 1: each slice of the reduction comes twice, for an operand in two parts
+  int a_part, b_part;   // where an operand's second part begins, from its first (0: the same again)
   int tiles_m, tiles_n;
   int splits, per_split;  // slices of a split
   int halved;             // tiles of each XCD that two workgroups share
@@ -239,15 +241,16 @@ struct Operand {
   int64_t ld;
   int ext, valid;   // by rows: reduction extent, output rows left; by columns: row extent
   int64_t K;        // reduction length
+  int two, part;    // GemmArgs
   int d0;           // by columns: first output index of the tile
   i32x4 rsrc;
   uint32_t off[LOADS];
   int chunk;        // by rows: this lane's logical chunk of a slice
 
   __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int64_t first,
-                                       int64_t count, int height, int ext_, int64_t K_, int wid,
-                                       int lane) {
-    ld = ld_, ext = ext_, K = K_;
+                                       int64_t count, int height, int ext_, int64_t K_, int two_,
+                                       int part_, int wid, int lane) {
+    ld = ld_, ext = ext_, K = K_, two = two_, part = part_;
     if constexpr (COLS) {
       base = p;
       d0 = static_cast<int>(first);
@@ -263,7 +266,7 @@ struct Operand {
     } else {
       base = p + first * ld;
       valid = static_cast<int>(min(int64_t(height), count - first));
-      rsrc = make_rsrc(base, (uint32_t(valid - 1) * uint32_t(ld) + uint32_t(ext)) * 2u);
+      rsrc = make_rsrc(base, (uint32_t(valid - 1) * uint32_t(ld) + uint32_t(part + ext)) * 2u);
       static_assert(WAVES * RPL % 32 == 0, "one key for all wave-loads");
       const int r0 = wid * RPL + lane / CPR;
       chunk = (lane % CPR) ^ row_key<BK>(r0);  // the other wave-loads start a multiple of 32 rows on: same key
@@ -278,7 +281,9 @@ struct Operand {
   // Slice kt's loads: by columns, the buffer range ends with the slice's last row;
   // by rows, a chunk past the reduction's end gets an offset outside. Slices
   // from `end` on read nothing but zeros (so that the loop has no last rounds
-  // of its own: such loads cost no memory traffic).
+  // of its own: such loads cost no memory traffic). With an operand in two parts,
+  // slices 2 k and 2 k + 1 are those of its parts at reduction slice k, so that
+  // the other operand's tile is read again while it is still in the caches.
   struct Slice {
     i32x4 rsrc;
     bool in;
@@ -286,15 +291,16 @@ struct Operand {
   };
   __device__ __forceinline__ Slice slice(int kt, int end) const {
     Slice s;
+    const int k = kt >> two, add = kt & two ? part : 0;
     if constexpr (COLS) {
-      const int rows = kt < end ? static_cast<int>(min(int64_t(BK), K - int64_t(kt) * BK)) : 0;
-      s.rsrc = make_rsrc(base + int64_t(kt) * BK * ld,
+      const int rows = kt < end ? static_cast<int>(min(int64_t(BK), K - int64_t(k) * BK)) : 0;
+      s.rsrc = make_rsrc(base + (int64_t(k) * BK * ld + add),
                          rows ? (uint32_t(rows - 1) * uint32_t(ld) + uint32_t(ext)) * 2u : 0u);
       s.in = true, s.advance = 0;
     } else {
       s.rsrc = rsrc;
-      s.in = kt < end && kt * BK + chunk * 8 < ext;
-      s.advance = uint32_t(kt) * (BK * 2);
+      s.in = kt < end && k * BK + chunk * 8 < ext;
+      s.advance = uint32_t(k) * (BK * 2) + uint32_t(add) * 2u;
     }
     return s;
   }
@@ -402,9 +408,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void linear_kernel(GemmArgs g) {
 
   OpA A;
   OpB B;
-  A.init(g.a, g.lda, m0, g.M, height, g.a_ext, g.K, wid, lane);
-  B.init(g.b, g.ldb, n0, g.N, BN, g.b_ext, g.K, wid, lane);
-  const int all = static_cast<int>((g.K + BK - 1) / BK);
+  A.init(g.a, g.lda, m0, g.M, height, g.a_ext, g.K, g.two, g.a_part, wid, lane);
+  B.init(g.b, g.ldb, n0, g.N, BN, g.b_ext, g.K, g.two, g.b_part, wid, lane);
+  const int all = static_cast<int>((g.K + BK - 1) / BK) << g.two;
   const int k0 = split * g.per_split, k1 = min(all, k0 + g.per_split);
   // Each XCD starts elsewhere in the reduction: rows a power-of-two-like stride
   // apart, all read at the same place at a time, would meet on a few memory

@@ -501,7 +501,8 @@ static int32_t linear_desc_status(const moe_linear_desc* d) {
       d->cols < 1 || d->cols > kDim)
     return MOE_ERR_ARG;
   if (d->w_order != MOE_W_NK && d->w_order != MOE_W_KN) return MOE_ERR_ARG;
-  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU) return MOE_ERR_ARG;
+  const int32_t act = d->act & ~MOE_DZ_16BIT;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_ERR_ARG;
   if (d->y_f32 != 0 && d->y_f32 != 1) return MOE_ERR_ARG;
   if (d->dtype != MOE_ROWS_BF16 && d->dtype != MOE_ROWS_F16) return MOE_ERR_UNSUPPORTED;
   const bool nk = d->w_order == MOE_W_NK;
@@ -559,7 +560,7 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
   if (st != MOE_OK || (!dx_d && !dw_d && !dbias_d)) return st;
   if (desc->rows > 0) {
     if (!dy_d) return MOE_ERR_ARG;
-    if (desc->act != MOE_ACT_NONE && (!pre_d || !row_stride_ok(desc->ldp, desc->cols)))
+    if ((desc->act & ~MOE_DZ_16BIT) != MOE_ACT_NONE && (!pre_d || !row_stride_ok(desc->ldp, desc->cols)))
       return MOE_ERR_ARG;
     if (dx_d && (!w_d || !aligned16(w_d))) return MOE_ERR_ARG;
     if (dw_d && (!x_d || !aligned16(x_d))) return MOE_ERR_ARG;

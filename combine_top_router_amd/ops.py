@@ -366,6 +366,7 @@ def grouped_swiglu(x_perm, offsets, counts, w1t, w3t, w2t, h=None, out=None):
 # ---------------------------------------------------------------- linear
 
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+_DZ_16BIT = 16
 _LINEAR_ROWS = {torch.bfloat16: 0, torch.float16: 1}
 
 
@@ -464,11 +465,13 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none", resid
 
 def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str = "none",
                     pre=None, want_dx: bool = True, want_dw: bool = True,
-                    want_dbias: bool = False, dx=None, dw=None, dbias=None, workspace=None):
+                    want_dbias: bool = False, dx=None, dw=None, dbias=None, workspace=None,
+                    dz16: bool = False):
     """(dx [M, K], dw [N, K], dbias [N] fp32) from dy [M, N] (as x, or fp32), None
     for those not wanted. ``pre`` is linear's pre-activation (for act other than
     "none"); dw lies in memory as w does. The residual's gradient is dy. No output
-    may share memory with a tensor of the call."""
+    may share memory with a tensor of the call. dy act'(pre) enters the products of
+    dx and dw as two 16-bit parts; with ``dz16`` as one, rounded, for half the work."""
     dev = x.device
     M, K = x.shape
     N = w.shape[0]
@@ -476,6 +479,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
         raise TypeError(f"dy must be {x.dtype} or fp32 (got {dy.dtype})")
     desc = _linear_desc(x, w, act, dy.dtype == torch.float32,
                         _need_rows(dy, "dy", dy.dtype, (M, N)))
+    desc.act |= _DZ_16BIT if dz16 else 0
     if act != "none":
         if pre is None:
             raise ValueError(f"act {act!r} needs the pre-activation")

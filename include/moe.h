@@ -479,6 +479,7 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
  */
 enum { MOE_W_NK = 0, MOE_W_KN = 1 };
 enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3 };
+enum { MOE_DZ_16BIT = 16 }; /* with act: moe_linear_backward's dz in one part (no effect on moe_linear) */
 
 typedef struct moe_linear_desc {
   int64_t rows;    /* M */
@@ -486,7 +487,7 @@ typedef struct moe_linear_desc {
   int32_t cols;    /* N */
   int32_t dtype;   /* MOE_ROWS_BF16 or MOE_ROWS_F16 */
   int32_t w_order; /* MOE_W_* */
-  int32_t act;     /* MOE_ACT_* */
+  int32_t act;     /* MOE_ACT_*, or with MOE_DZ_16BIT */
   int32_t y_f32;   /* 0: y (backward: dy) of dtype, 1: float */
   int64_t ldx, ldw, ldy, ldr, ldp;
 } moe_linear_desc;
@@ -503,17 +504,23 @@ int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d
  * moe_linear_backward -- gradients of moe_linear from dy [rows, cols] (of
  * dtype, or float with y_f32; row stride ldy) and the pre-activation:
  *
- *   dz = dy act'(pre)   fp32, then rounded to dtype for the two products (the
- *                       matrix cores read 16-bit values; this is the size of
- *                       the rounding the outputs have themselves); act' of an
- *                       infinite pre (z past fp16's range) is its limit
+ *   dz = dy act'(pre)   fp32; the matrix cores read 16-bit values, so the two products take
+ *                       it as two parts of dtype, dz rounded and what that leaves rounded:
+ *                       2^-16 of dz is lost in bf16, 2^-22 in fp16 (or 2^-25, if that is
+ *                       more). With act | MOE_DZ_16BIT as its first part alone, 2^-8 or
+ *                       2^-11 (nothing is lost of a dtype dy under act none or relu, which is
+ *                       one part anyway): half the products, and a second rounding of
+ *                       the size that dx and dw have themselves. act' of an infinite
+ *                       pre (z past fp16's range) is its limit
  *   dx = dz w           [rows, inner] of dtype, dense
  *   dw = dz^T x         in w's order, of dtype, dense
  *   dbias = column sums of the unrounded dz, [cols] float
  *
  * fp32 sums, one rounding per output; the residual's gradient is dy. dx_d,
  * dw_d and dbias_d may each be NULL to skip it. pre_d is needed unless act is none, w_d
- * for dx, x_d for dw. With fp16 rows, dz below fp16's range is lost: scale the loss.
+ * for dx, x_d for dw. With fp16 rows, dz below fp16's range is lost, and dz past 65504 is an
+ * infinity, also from a finite float dy, as are (or NaN) the row of dx and the row or column of
+ * dw that it reaches: scale the loss so that dz lies in between.
  * rows = 0 sets dw and dbias to zero. dx_d and dw_d 16-byte aligned; limits and
  * workspace as moe_linear, with moe_linear_backward_workspace_bytes.
  */

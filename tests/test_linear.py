@@ -144,3 +144,15 @@ def test_outputs_in_an_operand_are_refused():
             args = at[:7]
             args[out] = args[i]
             assert backward(*args) == 1
+
+
+@built
+def test_one_part_is_a_flag_beside_the_activation():
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    for act in range(4):
+        for call in (lib.moe_linear_workspace_bytes, lib.moe_linear_backward_workspace_bytes):
+            long = dict(inner=8192, ldx=8192, ldw=8192)
+            assert call(C.byref(_desc(act=act | 16, **long))) == call(C.byref(_desc(act=act, **long))) > 0
+    for act in (4 | 16, 32, 16 - 32):
+        assert lib.moe_linear_backward_workspace_bytes(C.byref(_desc(act=act))) == 0

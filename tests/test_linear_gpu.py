@@ -372,3 +372,85 @@ def test_sizes_past_32_bits_are_refused():
     x = torch.empty((1, 2 ** 32 + 8), dtype=BF, device="cuda")
     with pytest.raises(ValueError):
         ops.linear(x, x)
+
+
+def _pairs(gen, rows, cols, along):
+    """Random rows or columns, each twice in a row."""
+    v = torch.randn((rows // 2, cols) if along == 0 else (rows, cols // 2), generator=gen, device="cuda")
+    return v.repeat_interleave(2, dim=along)
+
+
+def _cancelling(gen, M, K, N, dtype, act, f32):
+    """dy, x, w, pre of which neighbouring rows' and columns' terms cancel but for 2^-6
+    of them: what a 16-bit dz loses of the terms then shows in dx and in dw."""
+    sign = 1.0 - 2.0 * ((torch.arange(M, device="cuda")[:, None] + torch.arange(N, device="cuda")) % 2)
+    base = torch.randn((M // 2, N // 2), generator=gen, device="cuda")
+    base = base.repeat_interleave(2, dim=0).repeat_interleave(2, dim=1)
+    dy = sign * base + 2.0 ** -6 * torch.randn((M, N), generator=gen, device="cuda")
+    x, w = _pairs(gen, M, K, 0).to(dtype), (_pairs(gen, N, K, 0) * K ** -0.5).to(dtype)
+    pre = None
+    if act != "none":
+        pre = torch.randn((M // 2, N // 2), generator=gen, device="cuda").repeat_interleave(2, dim=0)
+        pre = pre.repeat_interleave(2, dim=1).to(dtype)
+    return dy.to(torch.float32 if f32 else dtype), x, w, pre
+
+
+@pytest.mark.parametrize("shape", [(2, 8, 6), (64, 72, 64), (130, 136, 134), (1024, 64, 32),
+                                   (16, 7168, 256), (1030, 520, 776), (2050, 2056, 1032)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_gradients_lose_no_more_of_dz_than_its_two_parts(shape, dtype):
+    """dx and dw have their own rounding, and dz's are those of its second part: half a
+    step of half a step, u^2 of it (and fp16's smallest steps)."""
+    M, K, N = shape
+    gen = torch.Generator("cuda").manual_seed(M + N)
+    u = HALF_STEP[dtype]
+    for order in _orders(N):
+        for act, f32 in (("none", True), ("silu", False), ("gelu", True), ("relu", True)):
+            print("CASE dz", shape, dtype, order, act, f32, flush=True)
+            dy, x, w, pre = _cancelling(gen, M, K, N, dtype, act, f32)
+            wm = w if order == "nk" else w.t().contiguous().t()
+            dx, dw, _ = ops.linear_backward(dy, x, wm, act, pre)
+            torch.cuda.synchronize()
+            dys, xs, ws = f64(dy), f64(x), f64(w)
+            wx, ww, _, dz = olinear.linear_backward(dys, xs, ws, act, None if pre is None else f64(pre))
+            slope = 0.0 if act in ("none", "relu") else 2.0 ** -20 * np.abs(dys)
+            edz = slope + u * u * np.abs(dz) + TINY[dtype]
+            # twice the terms: sums of 2 n products, of magnitude dz and u dz
+            for got, want, mag, e, n in ((dx, wx, np.abs(dz) @ np.abs(ws), edz @ np.abs(ws), N),
+                                         (dw, ww, np.abs(dz).T @ np.abs(xs), edz.T @ np.abs(xs), M)):
+                e = e + (2 * n + 160) * 2.0 ** -23 * (1 + u) * mag
+                _close(got, want, e + u * (np.abs(want) + e) + TINY[dtype], "dx" if n == N else "dw")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_dz_in_one_part_is_dz_rounded(dtype):
+    gen = torch.Generator("cuda").manual_seed(21)
+    for M, K, N in ((40, 72, 24), (300, 264, 257), (600, 512, 1024)):
+        x, w = _matrix(gen, M, K, dtype), _matrix(gen, N, K, dtype, 0, K ** -0.5)
+        dy = _matrix(gen, M, N, torch.float32)
+        # (rounded before the call, dz is a 16-bit dy)
+        want = ops.linear_backward(dy.to(dtype), x, w)
+        got = ops.linear_backward(dy, x, w, dz16=True)
+        two = ops.linear_backward(dy, x, w)
+        torch.cuda.synchronize()
+        for a, b, c in zip(got[:2], want[:2], two[:2]):
+            assert torch.equal(a, b) and not torch.equal(a, c)
+        _backward(gen, M, K, N, dtype, "nk", "silu", True, dz16=True)
+
+
+def test_dz_past_fp16_is_an_infinity_in_its_row_and_column():
+    M, K, N = 20, 64, 16
+    gen = torch.Generator("cuda").manual_seed(22)
+    x, w = _matrix(gen, M, K, FP).abs() + 1, _matrix(gen, N, K, FP).abs() + 1
+    dy = _matrix(gen, M, N, torch.float32)
+    dx, dw, _ = ops.linear_backward(dy, x, w)
+    dy[3, 5] = 1e5
+    for dz16 in (False, True):
+        dx2, dw2, db = ops.linear_backward(dy, x, w, want_dbias=True, dz16=dz16)
+        torch.cuda.synchronize()
+        assert (dx2[3] == float("inf")).all() and (dw2[5] == float("inf")).all()
+        assert torch.isfinite(db).all()
+        if not dz16:
+            dx2[3], dw2[5] = dx[3], dw[5]
+            assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
