@@ -339,10 +339,13 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
     keep = in && place < a.top_groups;
     const float lowest = group_min<G>(keep ? rank : INFINITY);
     const float highest = group_max<G>(in && !keep ? rank : -INFINITY);
-    // (softmax: no score is above 1 / sum; not greater: infinities too are left to
-    // the exact choice)
+    // A rank's error: its scores', and half a step for each sum of fp32 values, of the
+    // two values' own size (which may cancel: a rank can be far smaller than they are). A
+    // rank of -inf is exact. (Softmax: no score is above 1 / sum; not greater:
+    // infinities too are left to the exact choice.)
+    const float terms = a.top2 && a.size > 1 ? fabsf(m1) + fabsf(m2) : fabsf(m1);
     const float off = a.sigmoid ? 0x1p-19f : (a.bias ? 0x1p-15f * inv : 0x1p-16f * lowest) + 0x1p-126f;
-    sure = lowest - highest > off + 0x1p-21f * (fabsf(lowest) + fabsf(highest));
+    sure = lowest - highest > off + 0x1p-20f * group_max<G>(in && rank > -INFINITY ? terms : 0.f);
   }
 
   // The k largest keys, and the one after them (unless there is no expert left). A

@@ -275,3 +275,41 @@ def test_arguments_past_32_bits_are_refused():
                 dict(num_groups=1 - 2 ** 32), dict(top_groups=2 ** 32 + 1)):
         with pytest.raises(ValueError):
             ops.route_scored(x, **{"top_k": 4, **bad})
+
+
+@pytest.mark.parametrize("B", [64.0, 1e4, 1e6])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_ranks_whose_two_values_cancel(B, score):
+    """Biases +B and -B inside each group: a rank is the sum of two values that are
+    rounded at B's size and leave one of the scores' size."""
+    T, E, groups, top = 100_000, 16, 8, 4
+    print("CASE cancel", B, score, flush=True)
+    gen = torch.Generator("cuda").manual_seed(int(B))
+    logits = torch.randn((T, E), generator=gen, device="cuda")
+    bias = torch.tensor([B, -B], device="cuda").repeat(E // 2)
+    _check(logits, 4, bias, score, groups, top, "top2", True, 1.0)
+    # one expert far above its group's other one, and a group of -inf beside
+    bias = torch.tensor([B, -1.0, B, -B, 0.5, -0.5, -float("inf"), 3.0] * 2, device="cuda")
+    _check(logits, 4, bias, score, groups, top, "top2", True, 1.0)
+
+
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[4] < s[3] and s[1] >= 2 * s[3]],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_close_group_ranks_are_told_apart_as_in_64_bits(shape, score):
+    """The best two of each group differ between groups by a few 2^-20 in the logits: ranks
+    from equal down to 2^-43 apart (pairs of equal sum), far above fp64's own rounding."""
+    T, E, k, groups, top = shape
+    print("CASE close ranks", shape, score, flush=True)
+    gen = torch.Generator("cuda").manual_seed(T + E)
+    size = E // groups
+    logits = torch.randn((T, groups, size), generator=gen, device="cuda") * 0.2 - 3
+    best = torch.rand((T, groups, size), generator=gen, device="cuda").topk(2, dim=2).indices
+    steps = torch.randint(0, 8, (T, groups, 2), generator=gen, device="cuda").float() * 2.0 ** -20
+    logits.scatter_(2, best, 1.5 + steps)
+    logits = logits.view(T, E).contiguous()
+    # one value for a group: sums of the same two scores stay equal in any order
+    bias = torch.randint(0, 4, (groups,), generator=gen, device="cuda").float() * 2.0 ** -21
+    for b in (None, bias.repeat_interleave(size).contiguous()):
+        for renorm in (True, False):
+            _check(logits, k, b, score, groups, top, "top2", renorm, 1.0)
