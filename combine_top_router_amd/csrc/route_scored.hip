@@ -471,10 +471,15 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
 //   softmax, renorm:    dl_j = scale * q_j (g_j - sum_i g_i q_i),  q the softmax of the selected logits
 //   softmax:            dl_e = scale * p_e (g_e [e selected] - sum_i g_i p_i),   every e
 //
+// The last one's difference cancels for an expert that holds nearly all of its
+// token: for a selected e it is formed as g_e (1 - p_e) - sum_{i != e} g_i p_i, with
+// 1 - p_e of the largest from the sum of the others' terms.
+//
 // G lanes own a token. Lane j < k forms slot j's value (sums over the slots
-// in fp64: they are few), the values are laid into an LDS row of E floats,
+// in fp64: they are few), the values are laid into an LDS row of E floats (over
+// the unselected experts' own, where every logit has a gradient),
 // and the lanes store the row four experts at a time. Bound by memory: 65536 tokens of
-// 256 experts, softmax over all: 27 us, 5.2 TB/s.
+// 256 experts, softmax over all: 28 us, 4.9 TB/s.
 struct RouteGradArgs {
   const float* logits;
   const int32_t* idx;
@@ -501,7 +506,7 @@ __global__ __launch_bounds__(kThreads) void route_scored_grad_kernel(RouteGradAr
                    (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 
   float l[kQ][4];
-  float lmax = -INFINITY, sum = 1.f;
+  float lmax = -INFINITY, sum = 1.f, rest = 0.f;  // rest: the terms of the sum that are not 1
   if (full) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
@@ -524,17 +529,21 @@ __global__ __launch_bounds__(kThreads) void route_scored_grad_kernel(RouteGradAr
     }
 #pragma unroll
     for (int off = G / 2; off >= 1; off >>= 1) lmax = fmaxf(lmax, __shfl_xor(lmax, off, kWave));
-    sum = 0.f;
+    float ones = 0.f;
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         l[q][u] = l[q][u] == -INFINITY ? 0.f : expf(l[q][u] - lmax);
-        sum += l[q][u];
+        (l[q][u] == 1.f ? ones : rest) += l[q][u];
       }
 #pragma unroll
-    for (int off = G / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, kWave);
-    if (sum == 0.f) sum = 1.f;
+    for (int off = G / 2; off >= 1; off >>= 1) {
+      ones += __shfl_xor(ones, off, kWave);
+      rest += __shfl_xor(rest, off, kWave);
+    }
+    sum = ones == 0.f ? 1.f : ones + rest;  // no expert has a finite logit: every score is 0
+    rest += ones - 1.f;  // beside one of the largest
   }
 
   // slot j: its score, its gradient, and what it puts at its expert
@@ -561,9 +570,9 @@ __global__ __launch_bounds__(kThreads) void route_scored_grad_kernel(RouteGradAr
     total += shfl_xor_f64(total, off);
     inner += shfl_xor_f64(inner, off);
   }
-  double d;
+  double d = 0.0;
   if (full) {
-    d = g;  // the row below scales it by the expert's own score
+    // from g and the others' g p, below
   } else if (a.sigmoid) {
     const double slope = ok ? p / (1.0 + exp(double(lj))) : 0.0;  // p (1 - p)
     d = (a.renorm ? (total == 0.0 ? 0.0 : (g - inner / total) / total) : g) * slope;
@@ -575,33 +584,53 @@ __global__ __launch_bounds__(kThreads) void route_scored_grad_kernel(RouteGradAr
   // a repeated expert takes the sum of its slots, in slot order, at the first of them
   double dsum = 0.0;
   bool first = true;
-  for (int i = 0; i < a.k; ++i) {
-    const int ei = __shfl(e, i, G);
-    const double di = __shfl(d, i, G);
-    if (ei == e) {
-      dsum += di;
-      if (i < j) first = false;
+  if (full) {
+    const float g32 = static_cast<float>(g), gp32 = static_cast<float>(g * p);
+    double others = 0.0;
+    for (int i = 0; i < a.k; ++i) {
+      const int ei = __shfl(e, i, G);
+      const float gi = __shfl(g32, i, G), gpi = __shfl(gp32, i, G);
+      if (ei == e) {
+        dsum += double(gi);
+        if (i < j) first = false;
+      } else {
+        others += double(gpi);
+      }
+    }
+    const bool one = lj > -INFINITY && expf(lj - lmax) == 1.f;
+    const double left = one ? double(rest / sum) : 1.0 - p;
+    dsum = double(a.scale) * p * (dsum * left - others);
+  } else {
+    for (int i = 0; i < a.k; ++i) {
+      const int ei = __shfl(e, i, G);
+      const double di = __shfl(d, i, G);
+      if (ei == e) {
+        dsum += di;
+        if (i < j) first = false;
+      }
     }
   }
 
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  const float factor = a.scale / sum, fi = static_cast<float>(inner);
 #pragma unroll
-  for (int q = 0; q < kQ; ++q)
-    if (j + q * G < chunks) tile[slot][j + q * G] = zero;
+  for (int q = 0; q < kQ; ++q) {
+    if (j + q * G >= chunks) continue;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (full) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = factor * l[q][u] * (0.f - fi);
+    }
+    tile[slot][j + q * G] = x;
+  }
   __syncthreads();
   if (ok && first) reinterpret_cast<float*>(tile[slot])[e] = static_cast<float>(dsum);
   __syncthreads();
   if (!live) return;
-  const float factor = a.scale / sum, fi = static_cast<float>(inner);
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
     const int c = j + q * G;
     if (c >= chunks) continue;
-    f32x4 x = tile[slot][c];
-    if (full) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) x[u] = factor * l[q][u] * (x[u] - fi);
-    }
+    const f32x4 x = tile[slot][c];
     float* o = a.out + t * E + 4 * c;
     if (vec) {
       __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(o));

@@ -313,3 +313,40 @@ def test_close_group_ranks_are_told_apart_as_in_64_bits(shape, score):
     for b in (None, bias.repeat_interleave(size).contiguous()):
         for renorm in (True, False):
             _check(logits, k, b, score, groups, top, "top2", renorm, 1.0)
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 8), (256, 8), (500, 16), (1024, 4)])
+@pytest.mark.parametrize("far", [3.0, 12.0, 18.0, 60.0])
+def test_softmax_gradient_of_a_confident_token(E, k, far):
+    """One expert holds nearly all of a token: dl_e = p_e (g_e (1 - p_e) - the others' g_i p_i),
+    every term of which p's own relative error bounds (g_e - inner would cancel)."""
+    T = 300
+    print("CASE confident", E, k, far, flush=True)
+    gen = torch.Generator("cuda").manual_seed(E + int(far))
+    logits = torch.randn((T, E), generator=gen, device="cuda") - far
+    best = torch.randint(0, E, (T, 1), generator=gen, device="cuda")
+    logits.scatter_(1, best, 0.5)
+    logits[1::3, 0] = logits[2::3, E - 1] = 0.5  # also two that share a token
+    idx, _ = ops.route_scored(logits, k, score="softmax", renormalise=False)
+    idx[0, 1] = idx[0, 0]  # and one that is named twice
+    g = torch.randn((T, k), generator=gen, device="cuda")
+    out = ops.route_scored_backward(logits, idx, g, "softmax", False, 1.5)
+    torch.cuda.synchronize()
+    l, gn, ix = logits.cpu().double().numpy(), g.cpu().double().numpy(), idx.cpu().long().numpy()
+    p = oscored.scores(l, "softmax")
+    G = np.zeros((T, E))
+    np.add.at(G, (np.arange(T)[:, None], ix), gn)
+    # 1 - p_e: the sum of the other scores
+    rest = np.stack([np.delete(p, e, axis=1).sum(axis=1) for e in range(E)], axis=1)
+    inner = G * p
+    others = np.stack([np.delete(inner, e, axis=1).sum(axis=1) for e in range(E)], axis=1)
+    want = 1.5 * p * (G * rest - others)
+    # (summed without e: as a total less e's own, 1 + 1e-26 - 1, the others would be lost)
+    size = np.stack([np.delete(np.abs(inner), e, axis=1).sum(axis=1) for e in range(E)], axis=1)
+    size = 1.5 * p * (np.abs(G) * rest + size)
+    size[0] += 1.5 * p[0] * p[0] * np.abs(gn[0]).max() * 2  # (the two named alike may cancel)
+    # each score: 32 half steps and 2 of |l - max|, as in _check_grad; two scores to a term,
+    # and the sum of the others, off by no more; the rest of the products 8
+    away = np.abs(l - l.max(axis=1, keepdims=True))
+    half_steps = 3 * 32 + 2 * away + 4 * away.max(axis=1, keepdims=True) + 8
+    _same(out, want, size * half_steps * U + 2.0 ** -126)
