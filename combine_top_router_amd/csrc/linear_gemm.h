@@ -78,17 +78,23 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-z));
 }
 
-// The normal distribution function by Abramowitz and Stegun 7.1.26 (absolute
-// error of erfc at most 1.5e-7): erfc(x) = t (a1 + t (a2 + ...)) e^(-x^2),
-// t = 1 / (1 + p x), x >= 0. The library's erfcf took a third of the time of a
+// The normal distribution function, by Hastings' form of the error function
+// (Abramowitz and Stegun 7.1.23-28), erfc(x) = t P(t) e^(-x^2), t = 1 / (1 + p x),
+// x >= 0, with eight terms fitted here to the relative error (1.1e-7 up to x = 10;
+// the book's five terms are within 1.5e-7 absolute, 0.16 % off at z = -5 and 2 % at -10).
+// With the hardware's exponential within 2^-21 (1 + z^2 / 2) of itself: about what half a
+// step of z does to it. The library's erfcf took a third of the time of a
 // 1023x4096x14336 product with gelu. g receives e^(-z^2/2).
 __device__ __forceinline__ float normal_cdf(float z, float& g) {
+  constexpr float kP[8] = {0.24252208f, 0.24425802f, 0.20570278f, 0.24429801f,
+                           -0.08078131f, 0.37818462f, -0.30707936f, 0.07289512f};
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.43f * x);
   g = __expf(-x * x);
-  const float half =
-      0.5f * g * t *
-      (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  float poly = kP[7];
+#pragma unroll
+  for (int i = 6; i >= 0; --i) poly = kP[i] + t * poly;
+  const float half = 0.5f * g * t * poly;
   return z < 0.f ? half : 1.f - half;
 }
 

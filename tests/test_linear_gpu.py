@@ -454,3 +454,37 @@ def test_dz_past_fp16_is_an_infinity_in_its_row_and_column():
         if not dz16:
             dx2[3], dw2[5] = dx[3], dw[5]
             assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_activations_to_their_relative_error(act, dtype):
+    """z known exactly (one product with 1): y within 2^-21 (1 + z^2 / 2) of itself for gelu,
+    2^-21 (2 + |z|) for silu, also where it is small; slopes of the size of their two terms."""
+    z = torch.cat([torch.linspace(-12.5, 12.5, 3001), torch.tensor([-0.0, 2.0 ** -14, -2.0 ** -14])])
+    z = z.to(dtype).cuda()
+    x = torch.zeros((z.numel(), 8), dtype=dtype, device="cuda")
+    x[:, 3] = z
+    w = torch.zeros((8, 8), dtype=dtype, device="cuda")
+    w[:, 3] = 1.0
+    zs = f64(z)[:, None]
+    want = np.repeat(olinear.act(zs, act), 8, axis=1)
+    rel = 2.0 ** -21 * (1 + zs * zs / 2 if act == "gelu" else 2 + np.abs(zs))
+    for t in (torch.float32, dtype):
+        y = ops.linear(x, w, act=act, out_dtype=t)
+        torch.cuda.synchronize()
+        _close(y, want, np.abs(want) * (rel + HALF_STEP[t]) * (1 + 2.0 ** -10) + TINY[t], str(t))
+    # one row: dbias is dz itself, fp32
+    n = z.numel() // 8 * 8
+    dy, pre = torch.ones((1, n), device="cuda"), z[:n].view(1, n)
+    _, _, db = ops.linear_backward(dy, x[:1], x[:n], act, pre, False, False, True)
+    torch.cuda.synchronize()
+    zs = f64(pre)[0]
+    slope = olinear.act_slope(zs, act)
+    if act == "gelu":
+        two = olinear._phi(zs) + np.abs(zs) * np.exp(-zs * zs / 2) / np.sqrt(2 * np.pi)
+        rel = 2.0 ** -21 * (1 + zs * zs / 2)
+    else:
+        s = 1 / (1 + np.exp(-zs))
+        two, rel = s * (1 + np.abs(zs)), 2.0 ** -21 * (2 + np.abs(zs))
+    _close(db, slope, two * (rel + 2.0 ** -22), "slope")
