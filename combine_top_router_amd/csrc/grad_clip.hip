@@ -198,7 +198,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(TensorTable t, const dou
   const double norm = sqrt(*sumsq);
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
   const double ratio = double(max_norm) / (norm + 1e-6);
-  const float coef = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);  // NaN stays NaN
+  // NaN stays NaN, but no bound leaves gradients of an infinite norm as they are
+  const float coef = ratio >= 1.0 || (isinf(norm) && isinf(max_norm)) ? 1.0f : static_cast<float>(ratio);
   const int total = t.first[t.n];
   // from the end backwards: what the norm's pass read last may still be in the caches
   for (int c = total - 1 - int(blockIdx.x); c >= 0; c -= gridDim.x) {

@@ -613,7 +613,8 @@ int32_t moe_route_backward(const int32_t* topk_idx_d, const float* topk_w_d,
  *
  * Two calls, so that ranks holding different parameters (expert parallelism)
  * can add their sums in between. A norm that is not finite gives what the
- * formula gives: coef NaN for a NaN norm, 0 for an infinite one. The order of the sum is
+ * formula gives: coef NaN for a NaN norm, 0 for an infinite one (1 if max_norm is
+ * infinite too: no bound). The order of the sum is
  * fixed by the tensors' order and sizes. In place, with coef = 1, nothing is written.
  *   tensors      HOST array of num_tensors descriptors, read during the call: `data` (device, aligned to
  *                its elements; may be NULL if numel is 0), `out` (moe_grad_clip: where the scaled

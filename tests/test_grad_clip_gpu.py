@@ -188,3 +188,17 @@ def test_captured_call_replays():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, out + [norm]))
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+def test_no_bound_leaves_gradients_of_an_infinite_norm(bad):
+    for dtype in (BF, FP, F32):
+        t = torch.tensor([1.0, bad, -3.0], dtype=dtype, device="cuda")
+        out = torch.zeros_like(t)
+        n = ops.clip_grad_norm([t], math.inf, out=[out])
+        m = ops.clip_grad_norm([t], math.inf)
+        torch.cuda.synchronize()
+        assert n.item() == m.item() == math.inf
+        assert t.tolist() == out.tolist() == [1.0, bad, -3.0]
+    t = torch.tensor([1.0, math.nan], device="cuda")  # a NaN norm reaches every element
+    assert math.isnan(ops.clip_grad_norm([t], math.inf).item()) and t.isnan().all()
