@@ -191,13 +191,15 @@ constexpr int BK = 64;  // reduction indexes of a slice
 // quiet chip, a slice where a second workgroup shares the compute unit (per_cu
 // 2), and a workgroup's beginning and end without its stores.
 struct Tile {
-  int bm, bn, per_cu;
+  int bm, bn, threads, per_cu;
   double slice, shared, fixed;
 };
 constexpr Tile kTiles[] = {
-    {256, 256, 1, 0.87, 0.0, 2.5},  {128, 256, 1, 0.55, 0.0, 2.9}, {128, 128, 2, 0.45, 1.35, 2.4},
-    {64, 128, 2, 0.30, 0.89, 2.4},  {64, 64, 2, 0.225, 0.59, 2.0}, {128, 128, 1, 0.375, 0.0, 2.5},
+    {256, 256, 512, 1, 0.87, 0.0, 2.5},   {128, 256, 512, 1, 0.55, 0.0, 2.9},
+    {128, 128, 256, 2, 0.45, 1.35, 2.4},  {64, 128, 256, 2, 0.30, 0.89, 2.4},
+    {64, 64, 256, 2, 0.225, 0.59, 2.0},   {128, 128, 512, 1, 0.375, 0.0, 2.5},
 };
+constexpr int64_t kLaunchThreads = (int64_t(1) << 32) - 1;
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128};
 
 struct Plan {
@@ -226,6 +228,8 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t cus) {
     for (const int want : kSplits) {
       if (want > 1 && want * 2 > all) break;
       const int64_t per = (all + want - 1) / want, s = (all + per - 1) / per, groups = tiles * s;
+      // what the launches take (cus: the most tiles that are halved)
+      if ((groups + cus) * c.threads > kLaunchThreads || (s > 1 && M * nw / 8 + 64 > kLaunchThreads)) break;
       const double out = double(std::min<int64_t>(c.bm, M)) * double(std::min<int64_t>(c.bn, N)) *
                          (s > 1 ? 4.0 : 2.0) / 3.45e6;  // one workgroup's stores, us
       const int64_t slots = cus * c.per_cu, full = groups / slots, rest = groups % slots;
@@ -277,6 +281,15 @@ Plan plan_product(int64_t M, int64_t N, int64_t K) {
   known[next] = {M, N, K, cus, p};
   next = (next + 1) % kKnown;
   return p;
+}
+
+// Whether a product's launch has fewer than 2^32 threads: false where no tile's would.
+bool launchable(int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_product(M, N, K);
+  const Tile& c = kTiles[p.tile];
+  const int64_t groups =
+      ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn) * p.splits + 8 * p.halved;
+  return groups * c.threads <= kLaunchThreads;
 }
 
 template <bool F16, bool AC, bool BC>
@@ -354,6 +367,16 @@ BackwardPlan plan_backward(const moe_linear_desc& d) {
 }
 
 }  // namespace
+
+bool linear_launchable(const moe_linear_desc& d) { return launchable(d.rows, d.cols, d.inner); }
+
+bool linear_backward_launchable(const moe_linear_desc& d) {
+  const int64_t M = d.rows, N = d.cols, K = d.inner;
+  const bool nk = d.w_order == MOE_W_NK;
+  const int64_t a = nk ? N : K, b = nk ? K : N;  // dw's rows and columns
+  return launchable(M, K, N) && launchable(M, K, two_parts(N)) && launchable(a, b, M) &&
+         launchable(a, b, two_parts(M));
+}
 
 size_t linear_workspace_bytes(const moe_linear_desc& d) {
   return static_cast<size_t>(plan_product(d.rows, d.cols, d.inner).part_bytes);

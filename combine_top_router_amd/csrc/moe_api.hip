@@ -511,18 +511,25 @@ static int32_t linear_desc_status(const moe_linear_desc* d) {
     return MOE_ERR_ARG;
   if (d->inner % 8 || d->ldx % 8 || d->ldw % 8 || (!nk && d->cols % 8))
     return MOE_ERR_UNSUPPORTED;
-  // a launch's workgroups (of at least 32 x 128 outputs) are counted in 32 bits
-  const int64_t big = std::max(d->inner, d->cols);
-  if ((d->rows / 128 + 1) * (big / 32 + 1) > (int64_t(1) << 31) / 512) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
+static int32_t linear_status(const moe_linear_desc* d) {
+  const int32_t st = linear_desc_status(d);
+  return st == MOE_OK && !moe::linear_launchable(*d) ? MOE_ERR_UNSUPPORTED : st;
+}
+
+static int32_t linear_backward_status(const moe_linear_desc* d) {
+  const int32_t st = linear_desc_status(d);
+  return st == MOE_OK && !moe::linear_backward_launchable(*d) ? MOE_ERR_UNSUPPORTED : st;
+}
+
 size_t moe_linear_workspace_bytes(const moe_linear_desc* desc) {
-  return linear_desc_status(desc) == MOE_OK ? moe::linear_workspace_bytes(*desc) : 0;
+  return linear_status(desc) == MOE_OK ? moe::linear_workspace_bytes(*desc) : 0;
 }
 
 size_t moe_linear_backward_workspace_bytes(const moe_linear_desc* desc) {
-  return linear_desc_status(desc) == MOE_OK ? moe::linear_backward_workspace_bytes(*desc) : 0;
+  return linear_backward_status(desc) == MOE_OK ? moe::linear_backward_workspace_bytes(*desc) : 0;
 }
 
 static bool workspace_ok(const void* ws, size_t have, size_t need) {
@@ -537,7 +544,7 @@ static bool clashes(const void* out, std::initializer_list<const void*> read) {
 int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d,
                    const float* bias_d, const void* residual_d, void* y_d, void* pre_d,
                    void* workspace_d, size_t workspace_bytes, void* stream) {
-  const int32_t st = linear_desc_status(desc);
+  const int32_t st = linear_status(desc);
   if (st != MOE_OK || desc->rows == 0) return st;
   if (!x_d || !w_d || !y_d || !aligned16(x_d) || !aligned16(w_d)) return MOE_ERR_ARG;
   if ((residual_d && !row_stride_ok(desc->ldr, desc->cols)) ||
@@ -556,7 +563,7 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
                             const void* w_d, const void* pre_d, void* dx_d, void* dw_d,
                             float* dbias_d, void* workspace_d, size_t workspace_bytes,
                             void* stream) {
-  const int32_t st = linear_desc_status(desc);
+  const int32_t st = linear_backward_status(desc);
   if (st != MOE_OK || (!dx_d && !dw_d && !dbias_d)) return st;
   if (desc->rows > 0) {
     if (!dy_d) return MOE_ERR_ARG;

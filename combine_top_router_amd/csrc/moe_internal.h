@@ -187,6 +187,9 @@ hipError_t launch_combine_backward(const void* grad_out, const void* y, int64_t 
 hipError_t launch_route_backward(const int32_t* topk_idx, const float* topk_w,
                                  const float* grad_w, int64_t T, int E, int k,
                                  float* grad_logits, hipStream_t s);
+// whether the launches of a call have fewer than 2^32 threads each
+bool linear_launchable(const moe_linear_desc& d);
+bool linear_backward_launchable(const moe_linear_desc& d);
 size_t linear_workspace_bytes(const moe_linear_desc& d);
 size_t linear_backward_workspace_bytes(const moe_linear_desc& d);
 hipError_t launch_linear(const moe_linear_desc& d, const void* x, const void* w,

@@ -472,9 +472,9 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
  * must not overlap (an output that begins where another buffer does is refused). Strides are in elements; ldr and ldp are read only where their buffer is given.
  * A masked row's values reach that row of y alone.
  * Limits: 0 <= rows < 2^31, 8 <= inner, 1 <= cols, both <= 2^20; dtype MOE_ROWS_BF16 or
- * MOE_ROWS_F16; inner, ldx and ldw multiples of 8; MOE_W_KN: cols a multiple of 8 too
- * and (rows / 128 + 1) * (max(inner, cols) / 32 + 1) <= 2^22 (else
- * MOE_ERR_UNSUPPORTED); strides at least the row length and at most 2^21.
+ * MOE_ROWS_F16 and inner, ldx and ldw multiples of 8, with MOE_W_KN cols too (else
+ * MOE_ERR_UNSUPPORTED); strides at least the row length and at most 2^21. A product of more
+ * tiles of 256 x 256 outputs than one launch takes, about 2^23, is MOE_ERR_UNSUPPORTED.
  *   workspace_d >= moe_linear_workspace_bytes(desc) bytes, 16-byte aligned (NULL if that
  *   is 0); contents on entry do not matter. Calls that may overlap need workspaces of their own.
  */

@@ -156,3 +156,18 @@ def test_one_part_is_a_flag_beside_the_activation():
             assert call(C.byref(_desc(act=act | 16, **long))) == call(C.byref(_desc(act=act, **long))) > 0
     for act in (4 | 16, 32, 16 - 32):
         assert lib.moe_linear_backward_workspace_bytes(C.byref(_desc(act=act))) == 0
+
+
+@built
+def test_products_of_more_tiles_than_a_launch_takes():
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    # 2^34 outputs are taken, whatever their shape; 2^40 are not, nor 2^23 tiles (of 512
+    # threads: 2^32, where a launch has fewer)
+    for rows, cols in ((1 << 20, 1 << 14), (1 << 14, 1 << 20), (1 << 30, 16)):
+        d = _desc(rows=rows, cols=cols, ldy=cols)
+        assert lib.moe_linear_backward_workspace_bytes(C.byref(d)) > 0, (rows, cols)
+    for rows, cols in ((1 << 20, 1 << 20), (1 << 30, 1 << 10), ((1 << 31) - 1, 8)):
+        d = _desc(rows=rows, cols=cols, ldy=cols)
+        assert lib.moe_linear(C.byref(d), C.c_void_p(1 << 20), C.c_void_p(1 << 21), None, None,
+                              C.c_void_p(1 << 22), None, None, 0, None) == 2, (rows, cols)

@@ -488,3 +488,28 @@ def test_activations_to_their_relative_error(act, dtype):
         s = 1 / (1 + np.exp(-zs))
         two, rel = s * (1 + np.abs(zs)), 2.0 ** -21 * (2 + np.abs(zs))
     _close(db, slope, two * (rel + 2.0 ** -22), "slope")
+
+
+def test_a_product_of_2_to_the_34_outputs():
+    M, K, N = 1 << 20, 64, 1 << 14  # 34 GB of outputs
+    gen = torch.Generator("cuda").manual_seed(23)
+    x, w = _matrix(gen, M, K, BF), _matrix(gen, N, K, BF, 0, K ** -0.5)
+    y = ops.linear(x, w)
+    rows = [0, 1, 255, 256, 131071, 131072, 524287, 524288, M - 257, M - 1]
+    torch.cuda.synchronize()
+    want, _ = olinear.linear(f64(x[rows]), f64(w))
+    e = (K + 160) * 2.0 ** -23 * (np.abs(f64(x[rows])) @ np.abs(f64(w)).T)
+    _close(y[rows], want, e + 2.0 ** -8 * (np.abs(want) + e), "y")
+    # and as a gradient: dx of the same rows, dw from a few rows alone
+    keep = y[rows].clone()
+    y.zero_()
+    y[rows] = keep
+    dx, dw, _ = ops.linear_backward(y, x, w)
+    torch.cuda.synchronize()
+    wx, ww, _, dz = olinear.linear_backward(f64(keep), f64(x[rows]), f64(w))
+    e = (N + 160) * 2.0 ** -23 * (np.abs(dz) @ np.abs(f64(w)))
+    _close(dx[rows], wx, e + 2.0 ** -8 * (np.abs(wx) + e), "dx")
+    e = 200 * 2.0 ** -23 * (np.abs(dz).T @ np.abs(f64(x[rows])))
+    _close(dw, ww, e + 2.0 ** -8 * (np.abs(ww) + e), "dw")
+    dx[rows] = 0
+    assert not dx.any()
