@@ -25,6 +25,7 @@ xtuner PR #2056, section "Design").
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
 
 import torch
@@ -45,6 +46,36 @@ class Router:
     scale: float = 1.0
 
 
+def _check(t, name: str, dtype, shape, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+
+
+def _check_router(r, num_experts: int, top_k: int, dev):
+    """What moe_route_scored would refuse, at the layer's construction."""
+    if not isinstance(r, Router):
+        raise TypeError("router must be a Router")
+    ops._one_of(ops._SCORES, r.score, "router.score")
+    ops._one_of(ops._RANKS, r.group_rank, "router.group_rank")
+    if not 1 <= r.num_groups <= 64 or num_experts % r.num_groups:
+        raise ValueError(f"router.num_groups must divide {num_experts} experts, 64 at most "
+                         f"(got {r.num_groups})")
+    if not 1 <= r.top_groups <= r.num_groups:
+        raise ValueError(f"router.top_groups must be 1 to {r.num_groups} (got {r.top_groups})")
+    if not 1 <= top_k <= r.top_groups * (num_experts // r.num_groups):
+        raise ValueError(f"top_k must be 1 to the experts of router.top_groups groups (got {top_k})")
+    if not math.isfinite(r.scale):
+        raise ValueError(f"router.scale must be finite (got {r.scale})")
+    if r.bias is not None:
+        _check(r.bias, "router.bias", torch.float32, (num_experts,), dev)
+
+
 class MoELayer:
     def __init__(self, num_tokens: int, hidden: int, num_experts: int, top_k: int, inter: int,
                  w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor, ep_size: int = 1,
@@ -60,6 +91,17 @@ class MoELayer:
             raise ValueError("a rank's share of the experts takes no shared expert: the sum over "
                              "the ranks would count it on each of them")
         dev = w1.device
+        if gate_w is not None:
+            _check(gate_w, "gate_w", torch.bfloat16, (num_experts, hidden), dev)
+        if router is not None:
+            _check_router(router, num_experts, top_k, dev)
+        if shared is not None:
+            if len(shared) != 3:
+                raise ValueError(f"shared must be (w1, w3, w2) (got {len(shared)} entries)")
+            width = shared[0].shape[-1] if isinstance(shared[0], torch.Tensor) else 0
+            for t, name, shape in zip(shared, ("w1", "w3", "w2"),
+                                      ((hidden, width), (hidden, width), (width, hidden))):
+                _check(t, f"shared {name}", torch.bfloat16, shape, dev)
         self.T, self.H, self.E, self.k, self.I = num_tokens, hidden, num_experts, top_k, inter
         self.desc = ops.layout_desc(num_tokens, num_experts, top_k, ep_size, local_rank, align)
         self.ep_size, self.local_rank, self.align = ep_size, local_rank, align
