@@ -218,20 +218,17 @@ __device__ __forceinline__ void finish_column(const Epilogue& e, const Block& b,
 }
 
 // Swizzle of a by-rows slice: the 16 rows that one LDS cycle reads at one
-// logical chunk must land on 16 different bank groups. Of 128-byte rows
-// (BK 64) a row's parity already picks one half of the banks, so the key is the
-// next three row bits; of 64-byte rows (BK 32) the row mod 4 picks a quarter.
-template <int BK>
-__device__ __forceinline__ int row_key(int row) {
-  return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
-}
+// logical chunk must land on 16 different bank groups. A 128-byte row's parity
+// already picks one half of the banks, so the key is the next three row bits.
+__device__ __forceinline__ int row_key(int row) { return (row >> 1) & 7; }
 
 // Swizzle of a by-columns slice with CPR 16-byte chunks to a row: the transposed
 // read's 32 lanes take 64 bytes of 4 consecutive rows, which have to lie in
 // different quarters of the banks.
 template <int CPR>
 __device__ __forceinline__ int col_key(int k) {
-  return CPR >= 16 ? (k & 3) << 2 : CPR == 8 ? ((k >> 1) & 1) << 2 : 0;
+  static_assert(CPR >= 8, "64 columns or more");
+  return CPR >= 16 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
 }
 
 // One operand's tile: D output indexes x BK reduction indexes.
@@ -242,6 +239,7 @@ struct Operand {
   static constexpr int RPL = 64 / CPR;          // LDS rows of a 1 KiB wave-load
   static constexpr int LOADS = BYTES / 1024 / WAVES;
   static_assert(LOADS * 1024 * WAVES == BYTES && LOADS >= 1, "whole wave-loads");
+  static_assert(BK == 64, "row_key is that of 128-byte rows");
 
   const uint16_t* base;
   int64_t ld;
@@ -275,7 +273,7 @@ struct Operand {
       rsrc = make_rsrc(base, (uint32_t(valid - 1) * uint32_t(ld) + uint32_t(part + ext)) * 2u);
       static_assert(WAVES * RPL % 32 == 0, "one key for all wave-loads");
       const int r0 = wid * RPL + lane / CPR;
-      chunk = (lane % CPR) ^ row_key<BK>(r0);  // the other wave-loads start a multiple of 32 rows on: same key
+      chunk = (lane % CPR) ^ row_key(r0);  // the other wave-loads start a multiple of 32 rows on: same key
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
         const int r = r0 + WAVES * RPL * i;
@@ -332,7 +330,7 @@ struct Operand {
       return __builtin_bit_cast(u32x4, v);
     } else {
       const int row = d + (lane & 31), ch = 2 * kk + (lane >> 5);
-      return *reinterpret_cast<const u32x4*>(s + row * (BK * 2) + ((ch ^ row_key<BK>(row)) << 4));
+      return *reinterpret_cast<const u32x4*>(s + row * (BK * 2) + ((ch ^ row_key(row)) << 4));
     }
   }
 };

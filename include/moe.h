@@ -94,8 +94,8 @@ int32_t moe_route(const float* logits_d, int64_t num_tokens, int32_t num_experts
  *
  * ties to the lower index. The choice is the one that fp64 scores, values and
  * ranks give: it does not depend on how an fp32 exponential rounds. The weights
- * are formed in fp32 (fp64 where a selected score would underflow). A NaN logit counts as -inf, +inf as the largest finite fp32; an
- * expert at -inf has score 0 and stays selectable. v = NaN (from the bias)
+ * are formed in fp32 (fp64 where a selected score would underflow). A NaN logit counts as
+ * -inf, +inf as the largest finite fp32; an expert at -inf has score 0 and stays selectable. v = NaN (from the bias)
  * counts as -inf. Renormalised weights whose sum is 0 are all 0.
  *
  *   logits_d    [T, E] float
@@ -126,7 +126,7 @@ int32_t moe_route_scored(const moe_route_desc* desc, const float* logits_d, cons
 /*
  * moe_route_scored_backward -- the gradient of moe_route_scored's weights
  * with respect to the logits, the choice held fixed (the bias has none), from
- * g = grad_w[t, :]. desc as in the forward; its groups are not used.
+ * g = grad_w[t, :]. desc as in the forward, within its limits; the groups change nothing.
  *
  *   sigmoid:              dl_j = scale * g_j s_j (1 - s_j)
  *   sigmoid, renormalise: dl_j = scale * (g_j - sum_i g_i s_i / S) / S * s_j (1 - s_j), S = sum_i s_i
@@ -469,7 +469,8 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
  *   y_d         [rows, cols] of `dtype` or (y_f32) float, row stride ldy (out)
  *   pre_d       [rows, cols] of `dtype`, row stride ldp, or NULL (out)
  * y may be the residual itself (same address, stride and type); other buffers
- * must not overlap (an output that begins where another buffer does is refused). Strides are in elements; ldr and ldp are read only where their buffer is given.
+ * must not overlap (an output that begins where another buffer does is refused). Strides
+ * are in elements; ldr and ldp are read only where their buffer is given.
  * A masked row's values reach that row of y alone.
  * Limits: 0 <= rows < 2^31, 8 <= inner, 1 <= cols, both <= 2^20; dtype MOE_ROWS_BF16 or
  * MOE_ROWS_F16 and inner, ldx and ldw multiples of 8, with MOE_W_KN cols too (else
