@@ -513,3 +513,42 @@ def test_a_product_of_2_to_the_34_outputs():
     _close(dw, ww, e + 2.0 ** -8 * (np.abs(ww) + e), "dw")
     dx[rows] = 0
     assert not dx.any()
+
+
+def _whole(gen, rows, cols, dtype, top):
+    """Random whole numbers of at most `top`."""
+    return torch.randint(-top, top + 1, (rows, cols), generator=gen, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("shape", SHAPES + [(4361, 2056, 4360), (1030, 7176, 4104), (2048, 8192, 512)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_whole_numbers_exactly(shape, dtype):
+    """Whole numbers whose sums fp32 holds (8192 terms of 3 * 3, of 900 * 2 with an fp32 dy's
+    4361: below 2^24): every term counts once, however it is split, and the one rounding is to even."""
+    M, K, N = shape
+    gen = torch.Generator("cuda").manual_seed(K)
+    for order in _orders(N):
+        print("CASE whole", shape, dtype, order, flush=True)
+        x, w = _whole(gen, M, K, dtype, 3), _whole(gen, N, K, dtype, 3)
+        wm = w if order == "nk" else w.t().contiguous().t()
+        b = _whole(gen, 1, N, torch.float32, 9)[0].contiguous()
+        r = _whole(gen, M, N, dtype, 9)
+        z = x.double() @ w.double().t() + b.double()
+        y, pre = z.relu() + r.double(), torch.empty((M, N), dtype=dtype, device="cuda")
+        assert torch.equal(ops.linear(x, wm, out_dtype=torch.float32), (z - b.double()).float())
+        assert torch.equal(ops.linear(x, wm, b, "relu", r, pre=pre), y.to(dtype))
+        assert torch.equal(pre, z.to(dtype))
+        assert torch.equal(ops.linear(x, wm, b, "relu", r, torch.float32), y.float())
+        # a 16-bit dy, and an fp32 one of more bits than one 16-bit part holds (900 * 2 of at
+        # most 4361 terms; dx and dw past fp16's range are infinite on both sides)
+        small = _whole(gen, M, N, dtype, 3)
+        big = _whole(gen, M, N, torch.float32, 900)
+        x, w = x.clamp(-2, 2), wm.clamp(-2, 2)
+        for dy in (small, big):
+            D = dy.double()
+            dx, dw, db = ops.linear_backward(dy, x, w, want_dbias=True)
+            torch.cuda.synchronize()
+            assert torch.equal(dx, (D @ w.double()).to(dtype))
+            assert torch.equal(dw, (D.t().contiguous() @ x.double()).to(dtype))
+            assert torch.equal(db, D.sum(dim=0).float())
