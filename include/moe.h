@@ -520,7 +520,8 @@ int32_t moe_linear(const moe_linear_desc* desc, const void* x_d, const void* w_d
  *
  * fp32 sums, one rounding per output; the residual's gradient is dy. dx_d,
  * dw_d and dbias_d may each be NULL to skip it. pre_d is needed unless act is none, w_d
- * for dx, x_d for dw. With fp16 rows, dz below fp16's range is lost, and dz past 65504 is an
+ * for dx, x_d for dw. An infinity in w or x makes what it reaches NaN where the second part's
+ * product with it is NaN or of the other sign. With fp16 rows, dz below fp16's range is lost, and dz past 65504 is an
  * infinity, also from a finite float dy, as are (or NaN) the row of dx and the row or column of
  * dw that it reaches: scale the loss so that dz lies in between.
  * rows = 0 sets dw and dbias to zero. dx_d and dw_d 16-byte aligned; limits and
