@@ -460,7 +460,7 @@ int32_t moe_grouped_down_wgrad(const void* h_d, const void* dy_d, const int32_t*
  *
  * act: none, relu, silu z / (1 + e^-z), or gelu z Phi(z) (Phi the normal
  * distribution function), within 2^-21 (2 + |z|) and 2^-21 (1 + z^2 / 2) of itself where it is
- * above fp32's smallest normal value. The router projection (fp32 logits from 16-bit
+ * above 2^-118 (and below that, within 2^-118). The router projection (fp32 logits from 16-bit
  * rows), a shared expert's products and dense layers.
  *   x_d         [rows, inner], row stride ldx;  w_d: MOE_W_NK [cols, inner] or MOE_W_KN
  *               [inner, cols], row stride ldw; both of `dtype`, 16-byte aligned

@@ -552,3 +552,20 @@ def test_whole_numbers_exactly(shape, dtype):
             assert torch.equal(dx, (D @ w.double()).to(dtype))
             assert torch.equal(dw, (D.t().contiguous() @ x.double()).to(dtype))
             assert torch.equal(db, D.sum(dim=0).float())
+
+
+def test_activations_of_very_negative_values():
+    """As above while the value is above 2^-118, and within 2^-118 below, down to -inf's side."""
+    z = torch.cat([torch.linspace(-86.0, -12.5, 500), torch.linspace(-3e4, -86.0, 500)]).to(BF).cuda()
+    x = torch.zeros((z.numel(), 8), dtype=BF, device="cuda")
+    x[:, 0] = z
+    w = torch.zeros((1, 8), dtype=BF, device="cuda")
+    w[:, 0] = 1.0
+    zs = f64(z)[:, None]
+    for act in ("silu", "gelu"):
+        y = ops.linear(x, w, act=act, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        with np.errstate(over="ignore"):
+            want = olinear.act(zs, act)
+        rel = 2.0 ** -21 * (1 + zs * zs / 2 if act == "gelu" else 2 + np.abs(zs)) + 2.0 ** -24
+        _close(y, want, np.where(np.abs(want) > 2.0 ** -118, np.abs(want) * rel, 2.0 ** -118), act)
