@@ -438,25 +438,19 @@ __global__ __launch_bounds__(kThreads) void route_scored_kernel(RouteArgs a) {
     ls = clean(row[my_e]);
   }
 
-  // The weights, from the selected logits: in fp32 where nothing underflows there.
-  float w = 0.f;
+  // The weights, from the selected logits, in fp64 up to their one rounding (an exponential
+  // a lane; in fp32 they were a second half step off, and 65536 tokens no faster).
+  // Only the softmax's sum over all experts is one of fp32 terms.
   float top = lmax;
   if (!a.sigmoid && a.renorm) top = group_max<G>(mine ? ls : -INFINITY);  // of the selected alone
-  const float x = a.sigmoid ? ls : ls - top;
-  if (__all(!mine || x > -80.f)) {
-    float s = 0.f;
-    if (mine) s = a.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x);
-    w = s / (a.renorm ? group_sum<G>(s) : sum) * a.scale;  // sum: 1 for the sigmoid
-  } else {
-    double s = 0.0;
-    if (mine && ls > -INFINITY)
-      s = a.sigmoid ? 1.0 / (1.0 + exp(-double(ls))) : exp(double(ls) - double(top));
-    double total = s;
+  double s = 0.0;
+  if (mine && ls > -INFINITY)
+    s = a.sigmoid ? 1.0 / (1.0 + exp(-double(ls))) : exp(double(ls) - double(top));
+  double total = s;
 #pragma unroll
-    for (int off = G / 2; off >= 1; off >>= 1) total += shfl_xor_f64(total, off);
-    if (!a.renorm) total = double(sum);
-    w = total == 0.0 ? 0.f : static_cast<float>(s / total * double(a.scale));
-  }
+  for (int off = G / 2; off >= 1; off >>= 1) total += shfl_xor_f64(total, off);
+  if (!a.renorm) total = double(sum);  // 1 for the sigmoid
+  const float w = total == 0.0 ? 0.f : static_cast<float>(s / total * double(a.scale));
   if (live && mine) {
     a.idx[t * a.k + j] = my_e;
     a.w[t * a.k + j] = w;

@@ -94,7 +94,7 @@ int32_t moe_route(const float* logits_d, int64_t num_tokens, int32_t num_experts
  *
  * ties to the lower index. The choice is the one that fp64 scores, values and
  * ranks give: it does not depend on how an fp32 exponential rounds. The weights
- * are formed in fp32 (fp64 where a selected score would underflow). A NaN logit counts as
+ * are formed in fp64 and rounded once (softmax without renormalise: over a sum of fp32 terms). A NaN logit counts as
  * -inf, +inf as the largest finite fp32; an expert at -inf has score 0 and stays selectable. v = NaN (from the bias)
  * counts as -inf. Renormalised weights whose sum is 0 are all 0.
  *

@@ -350,3 +350,19 @@ def test_softmax_gradient_of_a_confident_token(E, k, far):
     away = np.abs(l - l.max(axis=1, keepdims=True))
     half_steps = 3 * 32 + 2 * away + 4 * away.max(axis=1, keepdims=True) + 8
     _same(out, want, size * half_steps * U + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_weights_are_rounded_once(shape):
+    """Sigmoid weights, and renormalised softmax ones: fp64 up to half a step of fp32."""
+    T, E, k, groups, top = shape
+    print("CASE weights", shape, flush=True)
+    gen = torch.Generator("cuda").manual_seed(T * 31 + E)
+    logits = torch.randn((T, E), generator=gen, device="cuda") * 3
+    for score, renorm, scale in (("sigmoid", True, 2.5), ("sigmoid", False, 1.0),
+                                 ("softmax", True, 16.0), ("sigmoid", True, 0.3)):
+        idx, w = ops.route_scored(logits, k, None, score, groups, top, "max", renorm, scale)
+        torch.cuda.synchronize()
+        want = oscored.weights(logits.cpu().numpy(), idx.cpu().numpy(), score, renorm,
+                               np.float32(scale).item())
+        _same(w, want)
