@@ -41,6 +41,12 @@ class LinearDesc(C.Structure):
                 ("ldy", C.c_int64), ("ldr", C.c_int64), ("ldp", C.c_int64)]
 
 
+class NormDesc(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("hidden", C.c_int32), ("dtype", C.c_int32),
+                ("eps", C.c_float), ("reserved", C.c_int32), ("ldx", C.c_int64),
+                ("ldr", C.c_int64), ("ldt", C.c_int64), ("ldy", C.c_int64)]
+
+
 _P = C.c_void_p
 _I32, _I64, _SZ = C.c_int32, C.c_int64, C.c_size_t
 
@@ -78,6 +84,11 @@ SIGNATURES = {
     "moe_linear": (_I32, [C.POINTER(LinearDesc), _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_linear_backward": (_I32, [C.POINTER(LinearDesc), _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
                                    _P]),
+    "moe_rms_norm": (_I32, [C.POINTER(NormDesc), _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_rms_norm_backward_workspace_bytes": (_SZ, [C.POINTER(NormDesc)]),
+    "moe_rms_norm_backward": (_I32, [C.POINTER(NormDesc), _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_quantize_fp8": (_I32, [_I32, _P, _I64, _I32, _I64, _P, _P, _P]),
+    "moe_quantize_fp8_weights": (_I32, [_I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "moe_combine": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _P]),
     "moe_combine_backward": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
     "moe_permute_backward": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _P, _P]),

@@ -582,6 +582,116 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
                                                workspace_d, as_stream(stream)));
 }
 
+static bool rows_type(int32_t t) {
+  return t == MOE_ROWS_BF16 || t == MOE_ROWS_F16 || t == MOE_ROWS_F32;
+}
+
+// a row stride whose rows all start 16-byte aligned
+static bool wide_stride_ok(int64_t ld, int32_t n) { return row_stride_ok(ld, n) && ld % 8 == 0; }
+
+static int32_t norm_desc_status(const moe_norm_desc* d) {
+  if (!d || d->rows < 0 || d->rows >= (int64_t(1) << 31) || d->hidden < 8 || d->reserved ||
+      !(d->eps >= 0.f) || !std::isfinite(d->eps))
+    return MOE_ERR_ARG;
+  if (!rows_type(d->dtype) || d->hidden % 8 || d->hidden > kMaxHidden) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// `out` begins where `in` does without being it row for row
+static bool shifted(const void* out, int64_t ldo, const void* in, int64_t ldi) {
+  return out && out == in && ldo != ldi;
+}
+
+int32_t moe_rms_norm(const moe_norm_desc* desc, const void* x_d, const void* residual_d,
+                     const float* gain_d, void* total_d, void* y_d, void* q_d, float* scale_d,
+                     void* stream) {
+  const int32_t st = norm_desc_status(desc);
+  if (st != MOE_OK || desc->rows == 0) return st;
+  const int H = desc->hidden;
+  if (!x_d || (!total_d && !y_d && !q_d) || !q_d != !scale_d || (total_d && !residual_d))
+    return MOE_ERR_ARG;
+  if (!wide_stride_ok(desc->ldx, H) || (residual_d && !wide_stride_ok(desc->ldr, H)) ||
+      (total_d && !wide_stride_ok(desc->ldt, H)) || (y_d && !wide_stride_ok(desc->ldy, H)))
+    return MOE_ERR_ARG;
+  for (const void* p : {x_d, residual_d, static_cast<const void*>(gain_d),
+                        static_cast<const void*>(total_d), static_cast<const void*>(y_d),
+                        static_cast<const void*>(q_d), static_cast<const void*>(scale_d)})
+    if (!aligned16(p)) return MOE_ERR_ARG;
+  if (clashes(total_d, {gain_d, y_d}) || clashes(y_d, {gain_d}) ||
+      clashes(q_d, {x_d, residual_d, gain_d, total_d, y_d}) ||
+      clashes(scale_d, {x_d, residual_d, gain_d, total_d, y_d, q_d}) ||
+      shifted(total_d, desc->ldt, x_d, desc->ldx) ||
+      shifted(total_d, desc->ldt, residual_d, desc->ldr) ||
+      shifted(y_d, desc->ldy, x_d, desc->ldx) || shifted(y_d, desc->ldy, residual_d, desc->ldr))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_rms_norm(*desc, x_d, residual_d, gain_d, total_d, y_d, q_d, scale_d,
+                                        as_stream(stream)));
+}
+
+size_t moe_rms_norm_backward_workspace_bytes(const moe_norm_desc* desc) {
+  return norm_desc_status(desc) == MOE_OK ? moe::rms_norm_backward_workspace_bytes(*desc) : 0;
+}
+
+int32_t moe_rms_norm_backward(const moe_norm_desc* desc, const void* dy_d, const void* total_d,
+                              const float* gain_d, const void* dtotal_d, void* dx_d,
+                              float* dgain_d, void* workspace_d, size_t workspace_bytes,
+                              void* stream) {
+  const int32_t st = norm_desc_status(desc);
+  if (st != MOE_OK || (!dx_d && !dgain_d)) return st;
+  const int H = desc->hidden;
+  if (desc->rows > 0) {
+    if (!dy_d || !total_d || !wide_stride_ok(desc->ldy, H) || !wide_stride_ok(desc->ldx, H) ||
+        (dtotal_d && !wide_stride_ok(desc->ldt, H)) || (dx_d && !wide_stride_ok(desc->ldr, H)))
+      return MOE_ERR_ARG;
+  }
+  for (const void* p : {dy_d, total_d, static_cast<const void*>(gain_d), dtotal_d,
+                        static_cast<const void*>(dx_d), static_cast<const void*>(dgain_d)})
+    if (!aligned16(p)) return MOE_ERR_ARG;
+  if (clashes(dx_d, {gain_d}) || clashes(dgain_d, {dy_d, total_d, gain_d, dtotal_d, dx_d}) ||
+      shifted(dx_d, desc->ldr, dy_d, desc->ldy) || shifted(dx_d, desc->ldr, total_d, desc->ldx) ||
+      shifted(dx_d, desc->ldr, dtotal_d, desc->ldt))
+    return MOE_ERR_ARG;
+  if (dgain_d && !workspace_ok(workspace_d, workspace_bytes,
+                               moe::rms_norm_backward_workspace_bytes(*desc)))
+    return MOE_ERR_ARG;
+  if (desc->rows == 0 && !dgain_d) return MOE_OK;
+  return status_of(moe::launch_rms_norm_backward(*desc, dy_d, total_d, gain_d, dtotal_d, dx_d,
+                                                 dgain_d, workspace_d, as_stream(stream)));
+}
+
+int32_t moe_quantize_fp8(int32_t dtype, const void* x_d, int64_t rows, int32_t hidden, int64_t ldx,
+                         void* q_d, float* scale_d, void* stream) {
+  constexpr int32_t kDim = 1 << 20;
+  if (rows < 0 || hidden < 1 || hidden > kDim) return MOE_ERR_ARG;
+  if (!rows_type(dtype) || hidden % 8 || rows > ((int64_t(1) << 31) - 1) / ((hidden + 127) / 128))
+    return MOE_ERR_UNSUPPORTED;
+  if (!wide_stride_ok(ldx, hidden)) return MOE_ERR_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x_d || !q_d || !scale_d || !aligned16(x_d) || !aligned16(q_d) || !aligned16(scale_d) ||
+      clashes(q_d, {x_d, scale_d}) || clashes(scale_d, {x_d}))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_quantize_fp8(dtype, x_d, rows, hidden, ldx, q_d, scale_d,
+                                            as_stream(stream)));
+}
+
+int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mats, int32_t inner,
+                                 int32_t cols, int32_t w_order, void* q_d, float* scale_d,
+                                 void* stream) {
+  constexpr int32_t kDim = 1 << 20;
+  if (num_mats < 0 || num_mats >= 65536 || inner < 1 || inner > kDim || cols < 1 || cols > kDim ||
+      (w_order != MOE_W_NK && w_order != MOE_W_KN))
+    return MOE_ERR_ARG;
+  const bool turn = w_order == MOE_W_KN;
+  if (!rows_type(dtype) || inner % 16 || (turn && cols % 8)) return MOE_ERR_UNSUPPORTED;
+  if (num_mats == 0) return MOE_OK;
+  if (!w_d || !q_d || !scale_d || !aligned16(w_d) || !aligned16(q_d) || !aligned16(scale_d) ||
+      clashes(q_d, {w_d, scale_d}) || clashes(scale_d, {w_d}))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_quantize_fp8_weights(dtype, w_d, num_mats, turn ? inner : cols,
+                                                    turn ? cols : inner, turn, q_d, scale_d,
+                                                    as_stream(stream)));
+}
+
 static int32_t tensors_status(const moe_tensor_ref* t, int32_t n) {
   if (n < 0 || n > 65536 || (n > 0 && !t)) return MOE_ERR_ARG;
   for (int i = 0; i < n; ++i) {

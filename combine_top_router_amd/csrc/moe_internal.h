@@ -141,6 +141,7 @@ __device__ __forceinline__ void for_each_index(F&& f, std::integer_sequence<int,
 struct moe_route_desc;
 struct moe_linear_desc;
 struct moe_tensor_ref;
+struct moe_norm_desc;
 
 namespace moe {
 
@@ -241,6 +242,18 @@ hipError_t launch_grad_clip(const moe_tensor_ref* refs, int n, const double* sum
                             float* norm, hipStream_t s);
 // whether a written tensor shares memory with any other
 bool grad_clip_overlaps(const moe_tensor_ref* refs, int n);
+hipError_t launch_rms_norm(const moe_norm_desc& d, const void* x, const void* residual,
+                           const float* gain, void* total, void* y, void* q, float* scale,
+                           hipStream_t s);
+size_t rms_norm_backward_workspace_bytes(const moe_norm_desc& d);
+hipError_t launch_rms_norm_backward(const moe_norm_desc& d, const void* dy, const void* h,
+                                    const float* gain, const void* dtotal, void* dh, float* dgain,
+                                    void* ws, hipStream_t s);
+hipError_t launch_quantize_fp8(int dtype, const void* x, int64_t rows, int H, int64_t ldx, void* q,
+                               float* scale, hipStream_t s);
+// w: rows x cols as it lies in memory; turn: stored with its columns as rows
+hipError_t launch_quantize_fp8_weights(int dtype, const void* w, int mats, int rows, int cols,
+                                       bool turn, void* q, float* scale, hipStream_t s);
 size_t dispatch_layout_workspace_bytes(int64_t T, int E, int ep);
 hipError_t launch_dispatch_layout(const int32_t* idx, int64_t T, int E, int k, int ep,
                                   int32_t* per_rank, int32_t* per_expert, uint8_t* in_rank,

@@ -13,7 +13,7 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import LayoutDesc, LinearDesc, MoEError, RouteDesc, check, lib
+from ._lib import LayoutDesc, LinearDesc, MoEError, NormDesc, RouteDesc, check, lib
 
 
 def _stream(dev: torch.device):
@@ -501,6 +501,148 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
     _run(dev, "moe_linear_backward", d, dy.data_ptr(), x.data_ptr(), w.data_ptr(), _at(pre),
          _at(dx), _at(dw), _at(dbias), _at(ws), 0 if ws is None else ws.numel())
     return dx, dw, dbias
+
+
+# ---------------------------------------------------------------- norm, 8 bits
+
+_ROWS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_F8 = torch.float8_e4m3fn
+
+
+def _row_type(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in _ROWS:
+        raise TypeError(f"{name} must be bf16, fp16 or fp32 (got {t.dtype})")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix (got {tuple(t.shape)})")
+    return _ROWS[t.dtype]
+
+
+def _runs(n: int) -> int:
+    """Runs of 128 that share a scale."""
+    return (n + 127) // 128
+
+
+def rms_norm(x: torch.Tensor, gain=None, residual=None, eps: float = 1e-6, want_y: bool = True,
+             want_fp8: bool = False, y=None, q=None, scale=None, total=None):
+    """(y, q, scale, total), None for those not wanted: total = x + residual, rounded to
+    x's type (None without a residual), y = total / sqrt(mean(total^2) + eps) * gain in
+    x's type and, with ``want_fp8``, as e4m3 q [M, H] with scale [M, ceil(H / 128)]
+    fp32 (see quantize_fp8). x, residual [M, H] bf16, fp16 or fp32, gain [H] fp32.
+    ``total`` and ``y`` may each be x or the residual."""
+    t = _row_type(x, "x")
+    dev, dt = x.device, x.dtype
+    M, H = x.shape
+    _int32(H)
+    shape = (M, H)
+    desc = NormDesc(M, H, t, eps, 0, _need_rows(x, "x", dt, shape), 0, H, H)
+    if gain is not None:
+        _need(gain, "gain", torch.float32, (H,))
+    if residual is not None:
+        desc.ldr = _need_rows(residual, "residual", dt, shape)
+        if total is None:
+            total = torch.empty(shape, dtype=dt, device=dev)
+        else:
+            desc.ldt = _need_rows(total, "total", dt, shape)
+    elif total is not None:
+        raise ValueError("total needs a residual")
+    if not want_y:
+        y = None
+    elif y is None:
+        y = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        desc.ldy = _need_rows(y, "y", dt, shape)
+    if want_fp8:
+        q = _out(q, "q", _F8, shape, dev)
+        scale = _out(scale, "scale", torch.float32, (M, _runs(H)), dev)
+    else:
+        q = scale = None
+    _same_device(dev, gain, residual, total, y)
+    _run(dev, "moe_rms_norm", C.byref(desc), x.data_ptr(), _at(residual), _at(gain), _at(total),
+         _at(y), _at(q), _at(scale))
+    return y, q, scale, total
+
+
+def rms_norm_backward_workspace_bytes(total: torch.Tensor) -> int:
+    """Bytes of workspace ``rms_norm_backward`` needs on rows of this shape."""
+    M, H = total.shape
+    _int32(H)
+    return int(lib().moe_rms_norm_backward_workspace_bytes(
+        C.byref(NormDesc(M, H, _row_type(total, "total"), 0.0, 0, H, H, H, H))))
+
+
+def rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, gain=None, eps: float = 1e-6,
+                      dtotal=None, want_dx: bool = True, want_dgain: bool = True, dx=None,
+                      dgain=None, workspace=None):
+    """(dx [M, H] as total, dgain [H] fp32), None for those not wanted, from the gradient
+    dy of rms_norm's y and dtotal, what reaches ``total`` past the norm (None: nothing).
+    ``total`` is the forward's (its x, where it had no residual); dx is the gradient of
+    x and of the residual. ``dx`` may be dy, total or dtotal."""
+    t = _row_type(total, "total")
+    dev, dt = total.device, total.dtype
+    M, H = total.shape
+    _int32(H)
+    shape = (M, H)
+    desc = NormDesc(M, H, t, eps, 0, _need_rows(total, "total", dt, shape), H, 0,
+                    _need_rows(dy, "dy", dt, shape))
+    if gain is not None:
+        _need(gain, "gain", torch.float32, (H,))
+    if dtotal is not None:
+        desc.ldt = _need_rows(dtotal, "dtotal", dt, shape)
+    if not want_dx:
+        dx = None
+    elif dx is None:
+        dx = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        desc.ldr = _need_rows(dx, "dx", dt, shape)
+    dgain = _out(dgain, "dgain", torch.float32, (H,), dev) if want_dgain else None
+    _same_device(dev, dy, gain, dtotal, dx, workspace)
+    d = C.byref(desc)
+    ws = None
+    if want_dgain:
+        ws = _linear_workspace(lib().moe_rms_norm_backward_workspace_bytes(d), workspace, dev)
+    _run(dev, "moe_rms_norm_backward", d, dy.data_ptr(), total.data_ptr(), _at(gain), _at(dtotal),
+         _at(dx), _at(dgain), _at(ws), 0 if ws is None else ws.numel())
+    return dx, dgain
+
+
+def quantize_fp8(x: torch.Tensor, q=None, scale=None):
+    """(q [M, H] e4m3, scale [M, ceil(H / 128)] fp32) of rows x [M, H] bf16, fp16 or fp32:
+    each 128 columns of a row in units of scale = max(amax / 448, 2^-126), amax their
+    largest finite magnitude; what is not finite becomes NaN."""
+    t = _row_type(x, "x")
+    dev = x.device
+    M, H = x.shape
+    _int32(H)
+    ld = _need_rows(x, "x", x.dtype, (M, H))
+    q = _out(q, "q", _F8, (M, H), dev)
+    scale = _out(scale, "scale", torch.float32, (M, _runs(H)), dev)
+    _run(dev, "moe_quantize_fp8", t, x.data_ptr(), M, H, ld, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def quantize_fp8_weights(w: torch.Tensor, transpose: bool = False, q=None, scale=None):
+    """(q [.., N, K] e4m3, scale [.., ceil(N / 128), ceil(K / 128)] fp32) of weights w
+    [.., N, K], or with ``transpose`` [.., K, N] (math orientation), a matrix or a stack
+    of them, bf16, fp16 or fp32: a scale for each block of 128 x 128."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a tensor")
+    if w.dtype not in _ROWS:
+        raise TypeError(f"w must be bf16, fp16 or fp32 (got {w.dtype})")
+    if w.dim() not in (2, 3):
+        raise ValueError(f"w must be a matrix or a stack of matrices (got {tuple(w.shape)})")
+    _need(w, "w", w.dtype)
+    dev = w.device
+    lead = tuple(w.shape[:-2])
+    K, N = w.shape[-2:] if transpose else (w.shape[-1], w.shape[-2])
+    n = lead[0] if lead else 1
+    _int32(n, K, N)
+    q = _out(q, "q", _F8, lead + (N, K), dev)
+    scale = _out(scale, "scale", torch.float32, lead + (_runs(N), _runs(K)), dev)
+    _run(dev, "moe_quantize_fp8_weights", _ROWS[w.dtype], w.data_ptr(), n, K, N, int(transpose),
+         q.data_ptr(), scale.data_ptr())
+    return q, scale
 
 
 # ---------------------------------------------------------------- combine

@@ -533,6 +533,96 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
                             void* stream);
 
 /*
+ * moe_rms_norm -- the residual's addition and the root-mean-square norm.
+ *
+ *   total = x + residual      fp32, rounded to the rows' type (no residual: total = x)
+ *   y = total rstd gain       rstd = 1 / sqrt(mean(total^2) + eps), of the rounded total
+ *
+ * fp32 sums; y goes out rounded once to the rows' type and/or, unrounded, into 8 bits as
+ * moe_quantize_fp8 takes it. The norm in front of a layer: y for the router, q and its
+ * scales for the experts, total for the residual stream.
+ *   x_d         [rows, hidden] of `dtype`, row stride ldx
+ *   residual_d  [rows, hidden] of `dtype`, row stride ldr, or NULL
+ *   gain_d      [hidden] float, or NULL (ones)
+ *   total_d     [rows, hidden] of `dtype`, row stride ldt, or NULL (out; needs residual_d)
+ *   y_d         [rows, hidden] of `dtype`, row stride ldy, or NULL (out)
+ *   q_d         [rows, hidden] e4m3, dense, or NULL (out); scale_d [rows, ceil(hidden / 128)]
+ *               float, with q_d (out)
+ * total and y may each be x or the residual (same address and stride), not both the same one; other
+ * buffers must not overlap. A row whose sum of squares is past fp32's range gets rstd = 0, a NaN
+ * reaches its row alone. rows = 0 is a no-op.
+ * Limits: 0 <= rows < 2^31, hidden a multiple of 8, 8 <= hidden <= 16384, eps >= 0 and finite,
+ * dtype MOE_ROWS_*, strides multiples of 8 from hidden to 2^21, all buffers 16-byte aligned.
+ */
+typedef struct moe_norm_desc {
+  int64_t rows;
+  int32_t hidden;
+  int32_t dtype; /* MOE_ROWS_* */
+  float eps;
+  int32_t reserved; /* 0 */
+  int64_t ldx, ldr, ldt, ldy; /* elements; read only where their buffer is given */
+} moe_norm_desc;
+
+int32_t moe_rms_norm(const moe_norm_desc* desc, const void* x_d, const void* residual_d,
+                     const float* gain_d, void* total_d, void* y_d, void* q_d, float* scale_d,
+                     void* stream);
+
+/*
+ * moe_rms_norm_backward -- gradients of moe_rms_norm from those of y and total.
+ *
+ *   dx = rstd (gain dy - xhat mean(gain dy xhat)) + dtotal,   xhat = total rstd
+ *   dgain = sum over rows of dy xhat
+ *
+ * dx is the gradient of x and of the residual alike. fp32 (the rows' workgroups' dgain
+ * added in fp64, in order), one rounding per output.
+ *   dy_d      [rows, hidden] of `dtype`, row stride ldy
+ *   total_d   [rows, hidden] the forward's total (x, without a residual), row stride ldx
+ *   dtotal_d  [rows, hidden] what reaches total past the norm, row stride ldt, or NULL
+ *   dx_d      [rows, hidden], row stride ldr, or NULL (out); may be dy, total or dtotal
+ *             (same address and stride)
+ *   dgain_d   [hidden] float, or NULL (out); rows = 0 sets it to zero
+ *   workspace_d >= moe_rms_norm_backward_workspace_bytes(desc) bytes, 16-byte aligned, where dgain_d
+ *             is given; contents on entry do not matter
+ * Limits as moe_rms_norm.
+ */
+size_t moe_rms_norm_backward_workspace_bytes(const moe_norm_desc* desc);
+
+int32_t moe_rms_norm_backward(const moe_norm_desc* desc, const void* dy_d, const void* total_d,
+                              const float* gain_d, const void* dtotal_d, void* dx_d,
+                              float* dgain_d, void* workspace_d, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * 8-bit values: e4m3 (1 sign, 4 exponent, 3 fraction bits, largest 448, no infinity), with
+ * an fp32 scale s for each run of 128:
+ *
+ *   s = max(amax / 448, 2^-126),  q = e4m3(v (1 / s)),   v is held as q s
+ *
+ * amax is the largest magnitude among the run's finite values; a value that is not finite
+ * becomes NaN. fp32 operations, each rounded once, then one rounding (nearest even) to e4m3.
+ *
+ * moe_quantize_fp8: rows, a scale for each 128 columns (the last run may be shorter).
+ *   x_d [rows, hidden] of `dtype`, row stride ldx;  q_d [rows, hidden];
+ *   scale_d [rows, ceil(hidden / 128)] float (out)
+ * Limits: 0 <= rows, hidden a multiple of 8 from 8 to 2^20, rows * ceil(hidden / 128) < 2^31, ldx a
+ * multiple of 8 from hidden to 2^21.
+ *
+ * moe_quantize_fp8_weights: matrices, a scale for each block of 128 x 128 (the last ones
+ * may be smaller), stored output-major, as the products read them.
+ *   w_d     MOE_W_NK: [num_mats, cols, inner], MOE_W_KN: [num_mats, inner, cols], of `dtype`
+ *   q_d     [num_mats, cols, inner];  scale_d [num_mats, ceil(cols / 128), ceil(inner / 128)] (out)
+ * Limits: 0 <= num_mats < 65536, inner a multiple of 16 (MOE_W_KN: cols a multiple of 8), both
+ * from 1 to 2^20.
+ * All buffers 16-byte aligned; outputs must not overlap an input.
+ */
+int32_t moe_quantize_fp8(int32_t dtype, const void* x_d, int64_t rows, int32_t hidden, int64_t ldx,
+                         void* q_d, float* scale_d, void* stream);
+
+int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mats, int32_t inner,
+                                 int32_t cols, int32_t w_order, void* q_d, float* scale_d,
+                                 void* stream);
+
+/*
  * moe_combine -- fused weighted-sum restore.
  *
  * The fused restore of DeepSpeed PR #8847 ("AutoEP: support

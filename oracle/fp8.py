@@ -1,0 +1,95 @@
+"""Values in 8 bits (oracle): e4m3 and its scales.
+
+e4m3: 1 sign, 4 exponent (bias 7), 3 fraction bits; no infinity, the one NaN
+is all exponent and fraction bits set; largest value 448, smallest 2^-9.
+
+A run of 128 values (a row's columns) or of 128 x 128 (a weight matrix)
+shares s = max(amax / 448, 2^-126), amax its largest finite magnitude, and is
+held as e4m3(v (1 / s)): fp32 operations each rounded once, as the definition
+says, then one rounding to e4m3 (nearest, ties to even).
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def _table():
+    v = np.empty(256)
+    for b in range(256):
+        e, f = b >> 3 & 15, b & 7
+        m = f * 2.0 ** -9 if e == 0 else (8 + f) * 2.0 ** (e - 10)
+        v[b] = np.nan if b & 127 == 127 else -m if b & 128 else m
+    return v
+
+
+VALUES = _table()  # float64 value of each e4m3 byte
+
+
+def decode(b) -> np.ndarray:
+    """e4m3 bytes -> exact float64 values."""
+    return VALUES[np.asarray(b, np.uint8)]
+
+
+def encode(x) -> np.ndarray:
+    """float64 values -> e4m3 bytes: the nearest of the 127 magnitudes, ties to the
+    even byte; past the midpoint above 448, infinite and NaN: NaN."""
+    x = np.asarray(x, np.float64)
+    mags = VALUES[:127]
+    a = np.abs(x)
+    with np.errstate(invalid="ignore"):
+        hi = np.clip(np.searchsorted(mags, a), 1, 126)
+    lo = hi - 1
+    up, down = mags[hi] - a, a - mags[lo]
+    with np.errstate(invalid="ignore"):
+        b = np.where(up < down, hi, np.where(down < up, lo, np.where(hi % 2 == 0, hi, lo)))
+        b = np.where(a <= 464, b, 127)  # (464 is a tie: 448 is the even one)
+    return (b | np.where(np.signbit(x), 128, 0)).astype(np.uint8)
+
+
+def _quantize(v, amax):
+    """(bytes, s) of fp32 values v in units of s; amax broadcasts against v."""
+    s = np.maximum(amax.astype(np.float32) / np.float32(448), np.float32(2.0 ** -126))
+    r = np.float32(1) / s
+    with np.errstate(invalid="ignore", over="ignore"):
+        u = np.where(np.isfinite(v), v * r, np.float32(np.nan))
+    assert u.dtype == np.float32
+    return encode(u), s
+
+
+def rows(x):
+    """(bytes [M, H], s [M, ceil(H / 128)]) of fp32 rows."""
+    x = np.asarray(x, np.float32)
+    M, H = x.shape
+    n = -(-H // 128)
+    q, s = np.zeros((M, H), np.uint8), np.zeros((M, n), np.float32)
+    for j in range(n):
+        v = x[:, 128 * j:128 * j + 128]
+        amax = np.where(np.isfinite(v), np.abs(v), 0).max(axis=1, keepdims=True)
+        q[:, 128 * j:128 * j + 128], part = _quantize(v, amax)
+        s[:, j] = part[:, 0]
+    return q, s
+
+
+def weights(w):
+    """(bytes [N, K], s [ceil(N / 128), ceil(K / 128)]) of an fp32 matrix."""
+    w = np.asarray(w, np.float32)
+    N, K = w.shape
+    q = np.zeros((N, K), np.uint8)
+    s = np.zeros((-(-N // 128), -(-K // 128)), np.float32)
+    for i in range(s.shape[0]):
+        for j in range(s.shape[1]):
+            at = np.s_[128 * i:128 * i + 128, 128 * j:128 * j + 128]
+            amax = np.where(np.isfinite(w[at]), np.abs(w[at]), 0).max()
+            q[at], s[i, j] = _quantize(w[at], np.asarray(amax))
+    return q, s
+
+
+def row_values(q, s):
+    """What rows of bytes and their scales stand for, in float64."""
+    q = decode(q)
+    return q * np.repeat(np.asarray(s, np.float64), 128, axis=1)[:, :q.shape[1]]
+
+
+def weight_values(q, s):
+    """What a matrix of bytes and its scales stand for, in float64."""
+    return row_values(q, np.repeat(np.asarray(s), 128, axis=0)[:q.shape[0]])
