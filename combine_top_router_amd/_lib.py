@@ -47,6 +47,18 @@ class NormDesc(C.Structure):
                 ("ldr", C.c_int64), ("ldt", C.c_int64), ("ldy", C.c_int64)]
 
 
+class LinearFp8Desc(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("inner", C.c_int32), ("cols", C.c_int32),
+                ("dtype", C.c_int32), ("act", C.c_int32), ("y_f32", C.c_int32),
+                ("reserved", C.c_int32), ("ldy", C.c_int64), ("ldr", C.c_int64)]
+
+
+class GroupedFp8Desc(C.Structure):
+    _fields_ = [("m_cap", C.c_int64), ("max_rows", C.c_int64), ("num_tokens", C.c_int64),
+                ("num_groups", C.c_int32), ("inner", C.c_int32), ("cols", C.c_int32),
+                ("top_k", C.c_int32)]
+
+
 _P = C.c_void_p
 _I32, _I64, _SZ = C.c_int32, C.c_int64, C.c_size_t
 
@@ -89,6 +101,11 @@ SIGNATURES = {
     "moe_rms_norm_backward": (_I32, [C.POINTER(NormDesc), _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_quantize_fp8": (_I32, [_I32, _P, _I64, _I32, _I64, _P, _P, _P]),
     "moe_quantize_fp8_weights": (_I32, [_I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_linear_fp8_workspace_bytes": (_SZ, [C.POINTER(LinearFp8Desc)]),
+    "moe_linear_fp8": (_I32, [C.POINTER(LinearFp8Desc), _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_grouped_gate_up_fp8": (_I32, [C.POINTER(GroupedFp8Desc), _P, _P, _P, _P, _P, _P, _P, _P,
+                                       _P, _P, _P, _P]),
+    "moe_grouped_down_fp8": (_I32, [C.POINTER(GroupedFp8Desc), _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_combine": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _P]),
     "moe_combine_backward": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
     "moe_permute_backward": (_I32, [_P, _I64, _P, _I64, _I32, _I32, _P, _P]),

@@ -1,0 +1,751 @@
+// The tile kernel of the 8-bit products (fp8_gemm.hip has the whole picture):
+//   c[m, n] = sum over runs b of sa[m, b] sb[n / 128, b] sum over k in run b of a[m, k] w[n, k]
+#pragma once
+
+#include "fp8.h"
+#include "linear_epilogue.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16v8 __attribute__((ext_vector_type(8)));
+
+constexpr int kMaxGroups = 1024;
+constexpr int kWaves8 = 8;
+constexpr int kThreads8 = 64 * kWaves8;
+constexpr uint32_t kPast = 0x80000000u;  // a byte offset past every buffer range
+constexpr int kBandRows = 4;             // row tiles walked together
+constexpr int kDirectRows = 64;          // ragged: a group of so many rows is read straight into registers
+
+// kDense    one group of M rows, c through the linear layer's epilogue
+// kGrouped  ragged groups, each with a matrix of its own; c as kDense
+// kGated    ragged groups with two matrices: h = silu(a w0^T) * (a w1^T), in 8 bits with scales
+enum Kind8 { kDense = 0, kGrouped = 1, kGated = 2 };
+
+struct Fp8Args {
+  const uint8_t* a;        // [rows, K]
+  const float* sa;         // [rows, runs]
+  const uint8_t* w0;       // [groups, N, K]
+  const uint8_t* w1;       // kGated
+  const float* s0;         // [groups, ceil(N / 128), runs]
+  const float* s1;
+  int K, N, runs;
+  int64_t M;               // kDense: rows
+  const int32_t* offsets;  // ragged: [groups + 1], counts [groups]
+  const int32_t* counts;
+  int groups;
+  int64_t m_cap;           // no row at or past it is touched
+  int max_rows;            // rows of a group past it are not computed
+  const int32_t* gather;   // kGated, or nullptr: row r is a[gather[r] / top_k]
+  int top_k;
+  int64_t tokens;          // gather: rows of a
+  int tiles_m, tiles_n, splits, per_split;  // kDense
+  float* part;             // splits > 1: [splits, M, nw]
+  int64_t nw;
+  Epilogue e;              // kDense, kGrouped
+  uint8_t* h;              // kGated: [rows, N]
+  float* hs;               // [rows, N / 128]
+};
+
+// 4 bytes per lane, memory -> LDS, as dma16; four more wait states, for an offset that the
+// compiler restores from a spill right before it.
+__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
+               "{m0}"(lds_addr)
+               : "memory");
+}
+
+__device__ __forceinline__ i32x8 join(const u32x4& a, const u32x4& b) {
+  return i32x8{int(a[0]), int(a[1]), int(a[2]), int(a[3]), int(b[0]), int(b[1]), int(b[2]), int(b[3])};
+}
+
+// Eight e4m3 values as fp16, exactly.
+__device__ __forceinline__ f16v8 to_f16(int lo, int hi) {
+  const f16v2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+  const f16v2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+  const f16v2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+  const f16v2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+  return f16v8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// One run's products of 16 rows of w with 16 rows of a: lane l holds the columns
+// 4 (l / 16) .. + 3 (rows of w) of row l % 16. The K order inside the run does not matter,
+// as long as both operands have the same.
+// The 8-bit instruction adds each 8 neighbouring products after cutting them to multiples
+// of 2^-13 of the largest one's power of two (measured; the eights and the runs are added with 24
+// bits): 1.4e-5 of the result's norm on normal values, unbiased, far below an output of
+// 16 or 8 bits. EXACT goes through fp16, which holds every e4m3 value, at half the rate: its
+// sums keep 24 bits throughout (2e-7 a run). Taken for fp32 outputs, and where reading w is the bound.
+template <bool EXACT>
+__device__ __forceinline__ f32x4 run_product(const i32x8& w, const i32x8& a) {
+  if constexpr (EXACT) {
+    f32x4 c{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16(w[2 * q], w[2 * q + 1]),
+                                                 to_f16(a[2 * q], a[2 * q + 1]), c, 0, 0, 0);
+    return c;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0,
+                                                            0, 0);
+  }
+}
+
+__device__ __forceinline__ float silu8(float g) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+}
+
+// The order of a slice's products: row block by row block, the last two row blocks
+// together, so that a w fragment is free for the next slice's as soon as both have read it.
+constexpr int block_of(int p, int nb) { return p < (nb - 2) * 4 ? p / 4 : nb - 2 + ((p - (nb - 2) * 4) & 1); }
+constexpr int column_of(int p, int nb) { return p < (nb - 2) * 4 ? p % 4 : (p - (nb - 2) * 4) / 2; }
+
+// WIDE: rows of the outputs go out in 16-byte pieces (always so for the ragged kinds).
+// EXACT: run_product's
+template <int BM, int BN, int NS, int KIND, bool WIDE, bool EXACT>
+__global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
+  constexpr bool GATED = KIND == kGated, RAGGED = KIND != kDense;
+  constexpr int WN = BN / 64, WM = kWaves8 / WN, MB = BM / WM / 16;  // a wavefront: 16 MB rows x 64 staged columns
+  constexpr int OUT = GATED ? BN / 2 : BN;  // output columns of a tile
+  constexpr int A_BYTES = BM * kRun, B_BYTES = BN * kRun, S_BYTES = kThreads8 * 4;
+  constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
+  constexpr int AL = BM / 64, BL = BN / 64, NL = AL + BL + 1;  // wave-loads of a slice
+  constexpr int SW = BM / 64;  // the wavefront that brings w's scales; those before it bring the rows'
+  static_assert(MB >= 2 && MB % 2 == 0 && WM * WN == kWaves8 && SW + 1 < kWaves8, "tile");
+  __shared__ __attribute__((aligned(1024))) char smem[NS * STAGE];
+  // of each group: its rows, its first row, and the row tiles of the groups before it,
+  // those of more than kDirectRows rows in [0], the others' in [1]
+  __shared__ int mt_prefix[2][RAGGED ? kMaxGroups + 1 : 1], cnt_s[RAGGED ? kMaxGroups : 1],
+      off_s[RAGGED ? kMaxGroups : 1], wave_tot[2][kWaves8];
+  __shared__ uint32_t amax_s[GATED ? WN * BM : 1];
+
+  const int tid = threadIdx.x, lane = lane_id(), wid = uniform(tid / kWave);
+  const int wm = wid / WN, wn = wid % WN;
+  const int r15 = lane & 15, grp = lane >> 4;
+  const int K = g.K, N = g.N, KT = g.runs;
+  const int NT = (N + OUT - 1) / OUT;
+
+  int total, with_few = 0;  // tiles, and those with the groups of few rows behind them
+  if constexpr (RAGGED) {
+    // a group's rows stay inside [0, m_cap) whatever the device's counts say
+    constexpr int PER = kMaxGroups / kThreads8;
+    int v[2][PER], run[2] = {0, 0}, incl[2];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = tid * PER + q;
+      int c = 0;
+      if (e < g.groups) {
+        const int o = g.offsets[e];
+        const int64_t room = o < 0 ? 0 : max(int64_t(0), g.m_cap - o);
+        c = int(min(int64_t(min(max(g.counts[e], 0), g.max_rows)), room));
+        cnt_s[e] = c, off_s[e] = o;
+      }
+      v[0][q] = c > kDirectRows ? (c + BM - 1) / BM : 0;
+      v[1][q] = c > 0 && c <= kDirectRows ? 1 : 0;
+      run[0] += v[0][q], run[1] += v[1][q];
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      incl[z] = run[z];
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int o = __shfl_up(incl[z], off, kWave);
+        if (lane >= off) incl[z] += o;
+      }
+      if (lane == kWave - 1) wave_tot[z][wid] = incl[z];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      int ex = incl[z] - run[z];
+      for (int w = 0; w < wid; ++w) ex += wave_tot[z][w];
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int e = tid * PER + q;
+        if (e < g.groups) mt_prefix[z][e] = ex;
+        ex += v[z][q];
+      }
+      if (tid == kThreads8 - 1) mt_prefix[z][g.groups] = ex;
+    }
+    __syncthreads();
+    total = uniform(mt_prefix[0][g.groups]) * NT;
+    with_few = total + uniform(mt_prefix[1][g.groups]) * NT;
+  } else {
+    total = g.tiles_m * NT * g.splits;
+  }
+
+  const int G = gridDim.x;
+  int slot = blockIdx.x;
+  if ((G & 7) == 0) slot = (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3);
+
+  struct Tile {
+    int64_t row0;  // first row of a (without a gather) and of the outputs
+    int rows, n0, e, split;
+  };
+  // Tile ids run group by group, inside a group in bands of kBandRows row tiles, column tile
+  // major inside a band: the 32 neighbours of an XCD share the rows of 4 row tiles
+  // and the columns of 8 column tiles behind one L2.
+  auto locate = [&](int id, auto few) {
+    Tile t;
+    int mtiles, rem, rows;
+    if constexpr (RAGGED) {
+      const int* before = mt_prefix[decltype(few)::value];
+      int lo = 0, hi = g.groups - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] * NT <= id) lo = mid; else hi = mid - 1;
+      }
+      t.e = uniform(lo);
+      t.split = 0;
+      mtiles = uniform(before[t.e + 1] - before[t.e]);
+      rem = id - uniform(before[t.e]) * NT;
+      rows = uniform(cnt_s[t.e]);
+    } else {
+      const int tiles = g.tiles_m * NT;
+      t.e = 0;
+      t.split = id / tiles;
+      mtiles = g.tiles_m;
+      rem = id - t.split * tiles;
+      rows = 0;
+    }
+    const int full = mtiles / kBandRows * kBandRows;
+    int nt, mt;
+    if (rem < full * NT) {
+      const int band = rem / (kBandRows * NT), r2 = rem % (kBandRows * NT);
+      nt = r2 / kBandRows;
+      mt = band * kBandRows + r2 % kBandRows;
+    } else {
+      const int tail = mtiles - full, r2 = rem - full * NT;
+      nt = r2 / tail;
+      mt = full + r2 % tail;
+    }
+    t.n0 = nt * OUT;
+    if constexpr (RAGGED) {
+      // a group's 16-row blocks dealt out evenly: no short last tile
+      const int blks = (rows + 15) / 16, bq = blks / mtiles, br = blks % mtiles;
+      const int start = 16 * (mt * bq + min(mt, br));
+      t.rows = min((bq + (mt < br ? 1 : 0)) * 16, rows - start);
+      t.row0 = int64_t(uniform(off_s[t.e])) + start;
+    } else {
+      t.row0 = int64_t(mt) * BM;
+      t.rows = uniform(int(min(int64_t(BM), g.M - t.row0)));
+    }
+    return t;
+  };
+
+  // ---- operands of the current tile
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem));
+  // This lane's place in a wave-load of 8 rows x 128 bytes: row lane / 8, physical
+  // chunk lane % 8. The 16 rows that an LDS cycle reads at one logical chunk have to lie in
+  // 16 different bank groups; a row's parity picks a half of the banks, its key the
+  // chunk. a is read in runs of 16 rows, w in the rows 8 i + j and 8 i + 4 + j, i, j < 4.
+  const int ld_r = wid * 8 + lane / 8;
+  const int a_ch = (lane & 7) ^ ((ld_r >> 1) & 7);
+  const int b_ch = (lane & 7) ^ (((ld_r >> 1) & 1) | (((ld_r >> 3) & 3) << 1));
+  uint32_t oa[AL], ob[BL], osc;
+  i32x4 ra, rb0, rb1, rsc;
+
+  auto setup = [&](const Tile& t) {
+    const int64_t wrow = int64_t(t.e) * N + t.n0;
+    const int valid = min(OUT, N - t.n0);
+    const bool gathered = GATED && g.gather;
+    const int64_t a0 = gathered ? 0 : t.row0;
+    const uint32_t a_rows = gathered ? uint32_t(g.tokens) : uint32_t(t.rows);
+    // a row of the tile as a row of the range, or -1
+    auto source = [&](int r) {
+      if (r >= t.rows) return -1;
+      if (!gathered) return r;
+      const int src = g.gather[t.row0 + r];
+      const int token = src / g.top_k;
+      return src >= 0 && token < g.tokens ? token : -1;
+    };
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int r = source(ld_r + 64 * i);
+      oa[i] = r >= 0 ? uint32_t(r) * uint32_t(K) + uint32_t(a_ch) * 16u : kPast;
+    }
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int r = (ld_r + 64 * i) % OUT;
+      ob[i] = r < valid ? uint32_t(r) * uint32_t(K) + uint32_t(b_ch) * 16u : kPast;
+    }
+    ra = make_rsrc(g.a + a0 * K, a_rows * uint32_t(K));
+    rb0 = make_rsrc(g.w0 + wrow * K, uint32_t(valid) * uint32_t(K));
+    rb1 = GATED ? make_rsrc(g.w1 + wrow * K, uint32_t(valid) * uint32_t(K)) : rb0;
+    // scales: wavefronts before SW bring the rows', each wavefront row's MB blocks next to
+    // each other; SW those of w (two runs of columns, or w0's) and, gated, SW + 1 those of w1
+    osc = kPast;
+    if (wid < SW) {
+      const int s = wid * 64 + lane, w = s / MB;
+      const int r = source(((s % MB) * WM + w / 16) * 16 + (w & 15));
+      if (r >= 0) osc = uint32_t(r) * uint32_t(KT) * 4u;
+      rsc = make_rsrc(g.sa + a0 * KT, a_rows * uint32_t(KT) * 4u);
+    } else {
+      const int nblocks = (N + kRun - 1) / kRun;
+      const int left = min(GATED ? 1 : 2, nblocks - t.n0 / kRun);
+      const float* s = (GATED && wid > SW ? g.s1 : g.s0) + (int64_t(t.e) * nblocks + t.n0 / kRun) * KT;
+      rsc = make_rsrc(s, uint32_t(left) * uint32_t(KT) * 4u);
+      if (lane < left && wid <= SW + (GATED ? 1 : 0)) osc = uint32_t(lane) * uint32_t(KT) * 4u;
+    }
+  };
+  // wave-load q of slice kt into the stage at `at`; a slice at or past `end` reads nothing
+  // but zeros, as does a chunk past K
+  auto load = [&](auto q_tag, int kt, int end, uint32_t at) __attribute__((always_inline)) {
+    constexpr int q = decltype(q_tag)::value;
+    const int left = kt < end ? K - kt * kRun : 0;
+    if constexpr (q >= NL) {
+      return;
+    } else if constexpr (q < BL) {
+      dma16(GATED && q >= BL / 2 ? rb1 : rb0, b_ch * 16 < left ? ob[q] : kPast, uint32_t(kt) * kRun,
+            at + A_BYTES + (wid + kWaves8 * q) * 1024);
+    } else if constexpr (q < BL + AL) {
+      dma16(ra, a_ch * 16 < left ? oa[q - BL] : kPast, uint32_t(kt) * kRun,
+            at + (wid + kWaves8 * (q - BL)) * 1024);
+    } else {
+      dma4(rsc, left > 0 ? osc : kPast, uint32_t(kt) * 4u, at + A_BYTES + B_BYTES + wid * 256);
+    }
+  };
+  auto first_slices = [&](int k0, int k1) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      for_each_index([&](auto q) { load(q, k0 + s, k1, lds0 + s * STAGE); },
+                     std::make_integer_sequence<int, NL>{});
+  };
+
+  f32x4 acc[MB][4];
+
+  // The K loop on NB of the wavefront's row blocks (block i of the wavefront is block
+  // i WM + wm of the tile, so that a partly filled tile is shared out evenly).
+  auto kloop = [&](auto nb_tag, int k0, int k1) __attribute__((always_inline)) {
+    constexpr int NB = decltype(nb_tag)::value, NP = NB * 4, LAST = (NB - 2) * 4;
+    i32x8 fa[3], fb[4];  // block i's a fragment is in fa[(i + phase) % 3]
+    f32x4 part[4];
+    float sa[4], s_old[2], sb0, sb1;  // block i's row scale is in sa[i % 4]
+    // where this lane reads in the stage at hand: a's fragments (two halves; 16 rows on, 16 * 128
+    // bytes on), w's, and the rows' scales
+    int at_a = r15 * kRun + ((grp ^ (r15 >> 1)) << 4);
+    int at_b = A_BYTES + (8 * (r15 >> 2) + (r15 & 3)) * kRun +
+               ((grp ^ (((r15 >> 1) & 1) | ((r15 >> 2) << 1))) << 4);
+    int at_a2 = at_a ^ 64, at_b2 = at_b ^ 64;
+    int at_s = A_BYTES + B_BYTES + (wm * 16 + r15) * (MB * 4);
+    int at_w = A_BYTES + B_BYTES + BM * 4 + (GATED ? 0 : wn * 64 / kRun * 4);
+    asm volatile("" : "+v"(at_a), "+v"(at_b), "+v"(at_a2), "+v"(at_b2), "+v"(at_s));
+    auto read_a = [&](int i, int to) __attribute__((always_inline)) {
+      const int o = (i * WM + wm) * (16 * kRun);
+      fa[to] = join(*reinterpret_cast<const u32x4*>(smem + at_a + o),
+                    *reinterpret_cast<const u32x4*>(smem + at_a2 + o));
+    };
+    auto read_b = [&](int j) __attribute__((always_inline)) {
+      const int o = ((GATED ? (j >> 1) * OUT + wn * 32 : wn * 64 + (j >> 1) * 32) + 4 * (j & 1)) * kRun;
+      fb[j] = join(*reinterpret_cast<const u32x4*>(smem + at_b + o),
+                   *reinterpret_cast<const u32x4*>(smem + at_b2 + o));
+    };
+    auto read_sa = [&](int pair) __attribute__((always_inline)) {
+      const f32x2 v = *reinterpret_cast<const f32x2*>(smem + at_s + pair * 8);
+      sa[2 * (pair & 1)] = v[0], sa[2 * (pair & 1) + 1] = v[1];
+    };
+    auto read_sw = [&]() __attribute__((always_inline)) {
+      sb0 = *reinterpret_cast<const float*>(smem + at_w);
+      sb1 = GATED ? *reinterpret_cast<const float*>(smem + at_w + 256) : sb0;
+    };
+    wait_vmcnt<(NS - 1) * NL>();
+    __syncthreads();
+    read_sw();
+    read_sa(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < 2) read_a(j, j);
+      read_b(j);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) part[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    s_old[0] = s_old[1] = 0.f;
+    int stage = 0;
+    // One slice: each step is a product and the scaled addition of the product three
+    // steps before. All of the slice is read when the last two row blocks' products
+    // begin: the barrier there tells that it is by every wavefront and that the next
+    // slice has landed; the loads into the free stage and the reads of the next slice's
+    // first fragments go between those products, one each, or every
+    // wavefront's at once would fill the queues and hold up the products.
+    auto slice = [&](int kt, auto phase_tag) __attribute__((always_inline)) {
+      constexpr int PH = decltype(phase_tag)::value, PN = (PH + NB) % 3;
+      const uint32_t at = lds0 + stage * STAGE;
+      for_each_index([&](auto p_tag) __attribute__((always_inline)) {
+        constexpr int p = decltype(p_tag)::value, i = block_of(p, NB), j = column_of(p, NB);
+        if constexpr (p == LAST) {
+          wait_vmcnt<(NS - 2) * NL>();
+          __syncthreads();
+          // from here on the next stage is read
+          const bool wrap = stage + 1 == NS;
+          const int step = wrap ? -(NS - 1) * STAGE : STAGE;
+          stage = wrap ? 0 : stage + 1;
+          at_a += step, at_a2 += step, at_b += step, at_b2 += step, at_s += step, at_w += step;
+        }
+        // the product three steps back, of this slice or the last one
+        constexpr int o = p >= 3 ? p - 3 : NP - 3 + p;
+        constexpr int oi = block_of(o, NB), oj = column_of(o, NB);
+        const f32x4 old = part[o & 3];
+        float s;
+        if constexpr (p >= 3) s = sa[oi & 3] * (oj >= 2 ? sb1 : sb0);
+        else s = s_old[oi - (NB - 2)];
+        part[p & 3] = run_product<EXACT>(fb[j], fa[(i + PH) % 3]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[oi][oj][q] = __builtin_fmaf(old[q], s, acc[oi][oj][q]);
+        if constexpr (p < LAST) {
+          if constexpr (j == 0 && i + 2 < NB) read_a(i + 2, (i + 2 + PH) % 3);
+          if constexpr (j == 3 && i % 2 == 0 && i + 2 < NB) read_sa(i / 2 + 1);
+        } else {
+          constexpr int q = p - LAST;
+          load(std::integral_constant<int, q>{}, kt + NS, k1, at);
+          if constexpr (q == 7 && NL > 8) load(std::integral_constant<int, 8>{}, kt + NS, k1, at);
+          static_assert(NL <= 9, "loads fit the steps behind the barrier");
+          if constexpr (q == 0) read_a(0, PN);
+          if constexpr (q == 7) read_a(1, (1 + PN) % 3);
+          if constexpr (q & 1) read_b(q / 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }, std::make_integer_sequence<int, NP>{});
+      // the last three products are of columns 2 (block NB - 1) and 3
+      s_old[0] = sa[(NB - 2) & 3] * sb1;
+      s_old[1] = sa[(NB - 1) & 3] * sb1;
+      read_sw();
+      read_sa(0);
+    };
+    int kt = k0;
+    if constexpr (NB % 3 == 0) {
+      for (; kt < k1; ++kt) slice(kt, std::integral_constant<int, 0>{});
+    } else {
+      for (; kt + 2 < k1; kt += 3) {
+        slice(kt, std::integral_constant<int, 0>{});
+        slice(kt + 1, std::integral_constant<int, NB % 3>{});
+        slice(kt + 2, std::integral_constant<int, 2 * NB % 3>{});
+      }
+      if (kt < k1) slice(kt++, std::integral_constant<int, 0>{});
+      if (kt < k1) slice(kt, std::integral_constant<int, NB % 3>{});
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      constexpr int base = NP - 3;
+      const int oi = block_of(base + p, NB), oj = column_of(base + p, NB);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        acc[oi][oj][q] = __builtin_fmaf(part[(base + p) & 3][q], s_old[oi - (NB - 2)], acc[oi][oj][q]);
+    }
+  };
+
+  // ---- outputs
+  auto column_bias = [&](int64_t n, float (&bias)[8]) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) bias[q] = g.e.bias && n < N ? g.e.bias[n + q] : 0.f;
+  };
+  // A row's scale from its wavefronts' largest magnitudes, and its e4m3 values.
+  auto amax_row = [&](uint32_t m) {
+    m = max(m, uint32_t(__shfl_xor(int(m), 16, kWave)));
+    return max(m, uint32_t(__shfl_xor(int(m), 32, kWave)));
+  };
+
+  auto epilogue = [&](const Tile& t) {
+    // (hidden from the compiler, which would keep every block's addresses, all tiles long)
+    int r15 = lane & 15, grp = lane >> 4;
+    asm volatile("" : "+v"(r15), "+v"(grp));
+    if constexpr (GATED) {
+      float hv[MB][8];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        if ((i * WM + wm) * 16 >= t.rows) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) hv[i][q] = silu8(acc[i][q >> 2][q & 3]) * acc[i][2 + (q >> 2)][q & 3];
+        const uint32_t m = amax_row(magnitude(hv[i]));
+        if (grp == 0) amax_s[wn * BM + (i * WM + wm) * 16 + r15] = m;
+        __builtin_amdgcn_sched_barrier(0);  // one block's values at a time in registers
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const int r = (i * WM + wm) * 16 + r15;
+        if (r >= t.rows) continue;
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < WN; ++w) m = max(m, amax_s[w * BM + r]);
+        const float s = scale_of(m);
+        const int64_t row = t.row0 + r;
+        store_fp8x8(g.h, row * N + t.n0 + wn * 32 + grp * 8, to_fp8x8(hv[i], 1.f / s));
+        if (wn == 0 && grp == 0) g.hs[row * (N / kRun) + t.n0 / kRun] = s;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else if constexpr (WIDE) {
+      const bool parts = KIND == kDense && g.splits > 1;
+      const int64_t nw = t.n0 + wn * 64;
+      float bias[2][8];
+      if (!parts) {
+        column_bias(nw + grp * 8, bias[0]);
+        column_bias(nw + 32 + grp * 8, bias[1]);
+      }
+      const Block b(g.e, t.row0, nw);
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const int r = (i * WM + wm) * 16 + r15;
+        if ((i * WM + wm) * 16 >= t.rows) continue;
+        u32x4 res[2];
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int c = 32 * jj + 8 * grp;
+          if (!parts && g.e.res && r < t.rows && nw + c < N) res[jj] = load8x16(b.res + (int64_t(r) * g.e.ldr + c));
+        }
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int c = 32 * jj + 8 * grp;
+          if (r >= t.rows || nw + c >= N) continue;
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = acc[i][2 * jj + (q >> 2)][q & 3];
+          if (parts) {
+            float* p = g.part + (int64_t(t.split) * g.M + t.row0 + r) * g.nw + nw + c;
+            *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+          } else {
+            finish8(g.e, b, r, c, v, bias[jj], res[jj]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // one block's values at a time in registers
+      }
+    } else {
+      // rows of any alignment: a block of 16 rows x 64 columns through LDS, then a column to a lane
+      constexpr int ROW = 68;  // floats of an LDS row: rows 4 banks apart
+      float* ep = reinterpret_cast<float*>(smem) + wid * (16 * ROW);
+      const int64_t nw = t.n0 + wn * 64;
+      const int cols = int(min(int64_t(64), N - nw));
+      const float b1 = lane < cols && g.e.bias ? g.e.bias[nw + lane] : 0.f;
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const int rb = (i * WM + wm) * 16;
+        if (rb >= t.rows || cols <= 0) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<f32x4*>(ep + r15 * ROW + 32 * (j >> 1) + 8 * grp + 4 * (j & 1)) = acc[i][j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const Block b(g.e, t.row0 + rb, nw);
+#pragma unroll 1
+        for (int r = 0; r < 16; r += 8) {
+          float z[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) z[u] = ep[(r + u) * ROW + lane];
+          finish_column(g.e, b, r, 1, lane < cols ? min(16, t.rows - rb) : 0, lane, z, b1);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+    }
+  };
+
+  // A tile of few rows is bound by reading w, once: its wavefronts take 32 of the
+  // tile's w rows each and read them straight into registers, D runs ahead, with no barrier.
+  // RB: blocks of 16 rows.
+  auto direct = [&](const Tile& t, auto rb_tag, auto d_tag) {
+    constexpr int RB = decltype(rb_tag)::value, D = decltype(d_tag)::value;
+    const uint8_t *pw[2], *pa[RB];
+    const float* psa[RB];
+    const int nblocks = (N + kRun - 1) / kRun;
+    // plain: columns 32 wid + 8 grp .. + 7 in a lane; gated: gate and up columns 16 wid + 4 grp .. + 3
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int n = GATED ? wid * 16 + r15 : wid * 32 + 8 * (r15 >> 2) + (r15 & 3) + 4 * j;
+      const uint8_t* w = GATED && j ? g.w1 : g.w0;
+      pw[j] = w + (int64_t(t.e) * N + min(t.n0 + n, N - 1)) * K + grp * 16;
+    }
+    const int wb = min(t.n0 / kRun + (GATED ? 0 : wid * 32 / kRun), nblocks - 1);
+    const float* ps0 = g.s0 + (int64_t(t.e) * nblocks + wb) * KT;
+    const float* ps1 = GATED ? g.s1 + (int64_t(t.e) * nblocks + wb) * KT : ps0;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      // (rows past the tile's: the last one again; a row of a reaches its own outputs alone)
+      int64_t r = t.row0 + min(i * 16 + r15, t.rows - 1);
+      if (GATED && g.gather) {
+        const int src = g.gather[r];
+        r = src >= 0 ? min(int64_t(src / g.top_k), g.tokens - 1) : 0;
+      }
+      pa[i] = g.a + r * K + grp * 16;
+      psa[i] = g.sa + r * KT;
+    }
+    f32x4 sum[RB][2];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) sum[i][0] = sum[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Run {
+      u32x4 w[2][2], a[RB][2];
+      float sa[RB], s0, s1;
+    } ring[D];
+    auto fetch = [&](Run& x, int kt) __attribute__((always_inline)) {
+      const int k = min(kt, KT - 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) x.w[j][z] = *reinterpret_cast<const u32x4*>(pw[j] + k * kRun + z * 64);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) x.a[i][z] = *reinterpret_cast<const u32x4*>(pa[i] + k * kRun + z * 64);
+        x.sa[i] = psa[i][k];
+      }
+      x.s0 = ps0[k];
+      if constexpr (GATED) x.s1 = ps1[k];
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(ring[d], d);
+    for (int kt = 0; kt < KT; kt += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        Run& x = ring[d];
+        if (kt + d < KT) {
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const f32x4 p = run_product<true>(join(x.w[j][0], x.w[j][1]), join(x.a[i][0], x.a[i][1]));
+              const float s = x.sa[i] * (GATED && j ? x.s1 : x.s0);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) sum[i][j][q] = __builtin_fmaf(p[q], s, sum[i][j][q]);
+            }
+        }
+        fetch(x, kt + d + D);
+      }
+    }
+    if constexpr (GATED) {
+      float hv[RB][4];
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) hv[i][q] = silu8(sum[i][0][q]) * sum[i][1][q];
+        const uint32_t m = amax_row(magnitude(hv[i]));
+        if (grp == 0) amax_s[wid * (16 * RB) + i * 16 + r15] = m;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const int r = i * 16 + r15;
+        if (r >= t.rows) continue;
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves8; ++w) m = max(m, amax_s[w * (16 * RB) + r]);
+        const float s = scale_of(m);
+        const int64_t row = t.row0 + r;
+        const float v[8] = {hv[i][0], hv[i][1], hv[i][2], hv[i][3], 0.f, 0.f, 0.f, 0.f};
+        *reinterpret_cast<uint32_t*>(g.h + row * N + t.n0 + wid * 16 + grp * 4) = to_fp8x8(v, 1.f / s).x;
+        if (wid == 0 && grp == 0) g.hs[row * (N / kRun) + t.n0 / kRun] = s;
+      }
+    } else {
+      const int64_t nw = t.n0 + wid * 32;
+      const Block b(g.e, t.row0, nw);
+      float bias[8];
+      column_bias(nw + grp * 8, bias);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const int r = i * 16 + r15;
+        if (r >= t.rows || nw + grp * 8 >= N) continue;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = sum[i][q >> 2][q & 3];
+        finish8(g.e, b, r, grp * 8, v, bias, u32x4{0, 0, 0, 0});
+      }
+    }
+  };
+
+  // ---- the tiles
+  auto range = [&](const Tile& t, int& k0, int& k1) {
+    k0 = KIND == kDense ? t.split * g.per_split : 0;
+    k1 = KIND == kDense ? min(KT, k0 + g.per_split) : KT;
+  };
+  auto begin = [&](const Tile& t) {
+    int k0, k1;
+    range(t, k0, k1);
+    setup(t);
+    first_slices(k0, k1);
+  };
+  int id = slot;
+  if (id < total) {
+    Tile t = locate(id, std::integral_constant<int, 0>{});
+    begin(t);
+    for (;;) {
+      int k0, k1;
+      range(t, k0, k1);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int nb = ((t.rows + 15) / 16 + WM - 1) / WM;  // row blocks of a wavefront
+      constexpr int B4 = MB >= 8 ? MB - 4 : 2, B2 = MB >= 4 ? MB - 2 : 2;
+      if (MB >= 8 && nb <= B4) kloop(std::integral_constant<int, B4>{}, k0, k1);
+      else if (MB >= 4 && nb <= B2) kloop(std::integral_constant<int, B2>{}, k0, k1);
+      else kloop(std::integral_constant<int, MB>{}, k0, k1);
+      wait_vmcnt<0>();
+      __syncthreads();  // the stages are free
+      id += G;
+      if (id >= total) {
+        epilogue(t);
+        break;
+      }
+      const Tile now = t;
+      t = locate(id, std::integral_constant<int, 0>{});
+      if constexpr (WIDE) {
+        begin(t);  // the next tile's first slices are on their way during this one's epilogue
+        epilogue(now);
+      } else {
+        epilogue(now);
+        __syncthreads();  // LDS is read out before it is written again
+        begin(t);
+      }
+    }
+  }
+  if constexpr (RAGGED) {
+    for (; id < with_few; id += G) {
+      __syncthreads();  // amax_s is read out
+      const Tile t = locate(id - total, std::integral_constant<int, 1>{});
+      if (t.rows <= 16) direct(t, std::integral_constant<int, 1>{}, std::integral_constant<int, 6>{});
+      else if (t.rows <= 32) direct(t, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+      else direct(t, std::integral_constant<int, 4>{}, std::integral_constant<int, 3>{});
+    }
+  }
+}
+
+// The sums of the splits, in order, and the epilogue: eight columns a thread.
+__global__ __launch_bounds__(64) void fp8_join_kernel(Fp8Args g) {
+  const int64_t c8 = g.nw / 8;
+  const int64_t at = int64_t(blockIdx.x) * 64 + threadIdx.x;
+  if (at >= g.M * c8) return;
+  const int64_t m = at / c8, n = (at - m * c8) * 8;
+  const float* p = g.part + m * g.nw + n;
+  const int64_t step = g.M * g.nw;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int kBatch = 8;  // splits whose loads are in flight together
+  for (int s = 0; s < g.splits; s += kBatch) {
+    f32x4 x[kBatch], y[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (s + u < g.splits) {
+        x[u] = *reinterpret_cast<const f32x4*>(p + (s + u) * step);
+        y[u] = *reinterpret_cast<const f32x4*>(p + (s + u) * step + 4);
+      }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (s + u < g.splits) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += x[u][i], v[4 + i] += y[u][i];
+      }
+  }
+  const Block b(g.e, m, n);
+  if (g.e.vec && n + 8 <= g.N) {
+    float bias[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias[i] = g.e.bias ? g.e.bias[n + i] : 0.f;
+    finish8(g.e, b, 0, 0, v, bias, b.res ? load8x16(b.res) : u32x4{0, 0, 0, 0});
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float one[1] = {v[i]};
+      if (n + i < g.N) finish_column(g.e, b, 0, 1, 1, i, one, g.e.bias ? g.e.bias[n + i] : 0.f);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace moe

@@ -692,6 +692,88 @@ int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mat
                                                     as_stream(stream)));
 }
 
+static int32_t linear_fp8_status(const moe_linear_fp8_desc* d) {
+  constexpr int32_t kDim = 1 << 20;
+  if (!d || d->rows < 0 || d->rows >= (int64_t(1) << 31) || d->inner < 1 || d->inner > kDim ||
+      d->cols < 1 || d->cols > kDim || d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU ||
+      (d->y_f32 != 0 && d->y_f32 != 1) || d->reserved || !row_stride_ok(d->ldy, d->cols))
+    return MOE_ERR_ARG;
+  if ((d->dtype != MOE_ROWS_BF16 && d->dtype != MOE_ROWS_F16) || d->inner % 16 ||
+      !moe::linear_fp8_launchable(*d))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_linear_fp8_workspace_bytes(const moe_linear_fp8_desc* desc) {
+  return linear_fp8_status(desc) == MOE_OK ? moe::linear_fp8_workspace_bytes(*desc) : 0;
+}
+
+int32_t moe_linear_fp8(const moe_linear_fp8_desc* desc, const void* x_d, const float* x_scale_d,
+                       const void* w_d, const float* w_scale_d, const float* bias_d,
+                       const void* residual_d, void* y_d, void* workspace_d,
+                       size_t workspace_bytes, void* stream) {
+  const int32_t st = linear_fp8_status(desc);
+  if (st != MOE_OK || desc->rows == 0) return st;
+  if (!x_d || !x_scale_d || !w_d || !w_scale_d || !y_d || !aligned16(x_d) || !aligned16(w_d))
+    return MOE_ERR_ARG;
+  if (residual_d && !row_stride_ok(desc->ldr, desc->cols)) return MOE_ERR_ARG;
+  if (clashes(y_d, {x_d, x_scale_d, w_d, w_scale_d, bias_d})) return MOE_ERR_ARG;
+  if (residual_d == y_d && (desc->y_f32 || desc->ldr != desc->ldy)) return MOE_ERR_ARG;
+  if (!workspace_ok(workspace_d, workspace_bytes, moe::linear_fp8_workspace_bytes(*desc)))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_linear_fp8(*desc, x_d, x_scale_d, w_d, w_scale_d, bias_d, residual_d,
+                                          y_d, workspace_d, as_stream(stream)));
+}
+
+static int32_t grouped_fp8_status(const moe_grouped_fp8_desc* d, bool gather, int tile) {
+  constexpr int32_t kDim = 1 << 20;
+  if (!d || d->m_cap < 0 || d->max_rows < 0 || d->num_groups < 1 || d->num_groups > kMaxExperts ||
+      d->inner < 1 || d->inner > kDim || d->cols < 1 || d->cols > kDim)
+    return MOE_ERR_ARG;
+  if (gather && (d->num_tokens < 0 || d->top_k < 1 || d->top_k > kMaxTopK)) return MOE_ERR_ARG;
+  if (d->inner % 128 || d->cols % 128 || d->m_cap >= (int64_t(1) << 31) ||
+      (gather && d->num_tokens >= (int64_t(1) << 31) / d->inner) ||
+      (d->m_cap / 65 + d->num_groups) * ((d->cols + tile - 1) / tile) >= (int64_t(1) << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int32_t moe_grouped_gate_up_fp8(const moe_grouped_fp8_desc* desc, const void* x_d,
+                                const float* x_scale_d, const int32_t* src_row_d,
+                                const int32_t* offsets_d, const int32_t* counts_d,
+                                const void* w1_d, const float* w1_scale_d, const void* w3_d,
+                                const float* w3_scale_d, void* h_d, float* h_scale_d,
+                                void* stream) {
+  const int32_t st = grouped_fp8_status(desc, src_row_d != nullptr, 128);
+  if (st != MOE_OK || desc->m_cap == 0 || desc->max_rows == 0 || (src_row_d && desc->num_tokens == 0))
+    return st;
+  for (const void* p : {x_d, static_cast<const void*>(x_scale_d), w1_d,
+                        static_cast<const void*>(w1_scale_d), w3_d,
+                        static_cast<const void*>(w3_scale_d), static_cast<const void*>(h_d),
+                        static_cast<const void*>(h_scale_d)})
+    if (!p || !aligned16(p)) return MOE_ERR_ARG;
+  if (!offsets_d || !counts_d || clashes(h_d, {x_d, x_scale_d, w1_d, w1_scale_d, w3_d, w3_scale_d}) ||
+      clashes(h_scale_d, {x_d, x_scale_d, w1_d, w1_scale_d, w3_d, w3_scale_d, h_d}))
+    return MOE_ERR_ARG;
+  return status_of(moe::launch_gate_up_fp8(*desc, x_d, x_scale_d, src_row_d, offsets_d, counts_d, w1_d,
+                                           w1_scale_d, w3_d, w3_scale_d, h_d, h_scale_d,
+                                           as_stream(stream)));
+}
+
+int32_t moe_grouped_down_fp8(const moe_grouped_fp8_desc* desc, const void* h_d,
+                             const float* h_scale_d, const int32_t* offsets_d,
+                             const int32_t* counts_d, const void* w2_d, const float* w2_scale_d,
+                             void* y_d, void* stream) {
+  const int32_t st = grouped_fp8_status(desc, false, 256);
+  if (st != MOE_OK || desc->m_cap == 0 || desc->max_rows == 0) return st;
+  for (const void* p : {h_d, static_cast<const void*>(h_scale_d), w2_d,
+                        static_cast<const void*>(w2_scale_d), static_cast<const void*>(y_d)})
+    if (!p || !aligned16(p)) return MOE_ERR_ARG;
+  if (!offsets_d || !counts_d || clashes(y_d, {h_d, h_scale_d, w2_d, w2_scale_d})) return MOE_ERR_ARG;
+  return status_of(moe::launch_down_fp8(*desc, h_d, h_scale_d, offsets_d, counts_d, w2_d, w2_scale_d,
+                                        y_d, as_stream(stream)));
+}
+
 static int32_t tensors_status(const moe_tensor_ref* t, int32_t n) {
   if (n < 0 || n > 65536 || (n > 0 && !t)) return MOE_ERR_ARG;
   for (int i = 0; i < n; ++i) {

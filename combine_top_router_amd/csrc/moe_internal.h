@@ -142,6 +142,8 @@ struct moe_route_desc;
 struct moe_linear_desc;
 struct moe_tensor_ref;
 struct moe_norm_desc;
+struct moe_linear_fp8_desc;
+struct moe_grouped_fp8_desc;
 
 namespace moe {
 
@@ -254,6 +256,18 @@ hipError_t launch_quantize_fp8(int dtype, const void* x, int64_t rows, int H, in
 // w: rows x cols as it lies in memory; turn: stored with its columns as rows
 hipError_t launch_quantize_fp8_weights(int dtype, const void* w, int mats, int rows, int cols,
                                        bool turn, void* q, float* scale, hipStream_t s);
+size_t linear_fp8_workspace_bytes(const moe_linear_fp8_desc& d);
+bool linear_fp8_launchable(const moe_linear_fp8_desc& d);
+hipError_t launch_linear_fp8(const moe_linear_fp8_desc& d, const void* x, const float* sx,
+                             const void* w, const float* sw, const float* bias,
+                             const void* residual, void* y, void* ws, hipStream_t s);
+hipError_t launch_gate_up_fp8(const moe_grouped_fp8_desc& d, const void* x, const float* sx,
+                              const int32_t* src_row, const int32_t* offsets,
+                              const int32_t* counts, const void* w1, const float* s1,
+                              const void* w3, const float* s3, void* h, float* hs, hipStream_t s);
+hipError_t launch_down_fp8(const moe_grouped_fp8_desc& d, const void* h, const float* hs,
+                           const int32_t* offsets, const int32_t* counts, const void* w2,
+                           const float* s2, void* y, hipStream_t s);
 size_t dispatch_layout_workspace_bytes(int64_t T, int E, int ep);
 hipError_t launch_dispatch_layout(const int32_t* idx, int64_t T, int E, int k, int ep,
                                   int32_t* per_rank, int32_t* per_expert, uint8_t* in_rank,

@@ -13,7 +13,9 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import LayoutDesc, LinearDesc, MoEError, NormDesc, RouteDesc, check, lib
+from ._lib import (
+    GroupedFp8Desc, LayoutDesc, LinearDesc, LinearFp8Desc, MoEError, NormDesc, RouteDesc, check, lib,
+)
 
 
 def _stream(dev: torch.device):
@@ -643,6 +645,127 @@ def quantize_fp8_weights(w: torch.Tensor, transpose: bool = False, q=None, scale
     _run(dev, "moe_quantize_fp8_weights", _ROWS[w.dtype], w.data_ptr(), n, K, N, int(transpose),
          q.data_ptr(), scale.data_ptr())
     return q, scale
+
+
+def _need_fp8(q, scale, name: str, shape, blocks):
+    """Checks an e4m3 tensor and its scales."""
+    _need(q, name, _F8, shape)
+    _need(scale, name + "_scale", torch.float32, blocks)
+
+
+def _linear_fp8_desc(x, w, act: str, dt, res_dt=None) -> LinearFp8Desc:
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    if dt not in _ROWS:
+        raise TypeError(f"out must be bf16, fp16 or fp32 (got {dt})")
+    if res_dt is not None and (res_dt not in _LINEAR_ROWS or dt not in (res_dt, torch.float32)):
+        raise TypeError(f"residual must be bf16 or fp16, and of out's type or below an fp32 out "
+                        f"(got {res_dt} and {dt})")
+    M, K = x.shape
+    N = w.shape[0]
+    _int32(K, N)
+    f32 = dt == torch.float32
+    t = _LINEAR_ROWS[res_dt if res_dt is not None else torch.bfloat16 if f32 else dt]
+    return LinearFp8Desc(M, K, N, t, _one_of(_ACTS, act, "act"), int(f32), 0, N, 0)
+
+
+def linear_fp8_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
+    """Bytes of workspace ``linear_fp8`` needs on these operands (often 0)."""
+    return int(lib().moe_linear_fp8_workspace_bytes(
+        C.byref(_linear_fp8_desc(x, w, "none", torch.bfloat16))))
+
+
+def linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+               bias=None, act: str = "none", residual=None, out_dtype=None, out=None,
+               workspace=None) -> torch.Tensor:
+    """act(x w^T + bias) + residual on 8-bit operands: x [M, K] e4m3 with x_scale
+    [M, ceil(K / 128)] (quantize_fp8, rms_norm), w [N, K] e4m3 with w_scale
+    [ceil(N / 128), ceil(K / 128)] (quantize_fp8_weights), bias [N] fp32, residual [M, N]
+    bf16 or fp16; the result bf16 (the default), fp16 or fp32. ``out`` may be
+    ``residual``. fp32 sums, one rounding. The gradient of x is the same call on the
+    transposed weights."""
+    dev = x.device
+    dt = out.dtype if out is not None else torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype is not None and dt != out_dtype:
+        raise TypeError(f"out must be {out_dtype} (got {dt})")
+    desc = _linear_fp8_desc(x, w, act, dt, None if residual is None else residual.dtype)
+    M, K, N = desc.rows, desc.inner, desc.cols
+    _need_fp8(x, x_scale, "x", (M, K), (M, _runs(K)))
+    _need_fp8(w, w_scale, "w", (N, K), (_runs(N), _runs(K)))
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=dev)
+    else:
+        desc.ldy = _need_rows(out, "out", dt, (M, N))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (N,))
+    if residual is not None:
+        desc.ldr = _need_rows(residual, "residual", residual.dtype, (M, N))
+    _same_device(dev, x_scale, w, w_scale, bias, residual, out, workspace)
+    d = C.byref(desc)
+    ws = _linear_workspace(lib().moe_linear_fp8_workspace_bytes(d), workspace, dev)
+    _run(dev, "moe_linear_fp8", d, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
+         w_scale.data_ptr(), _at(bias), _at(residual), out.data_ptr(), _at(ws),
+         0 if ws is None else ws.numel())
+    return out
+
+
+def _grouped_fp8(rows, offsets, counts, w, m_cap: int, max_rows, name: str):
+    """(descriptor, group count, rows' width, outputs' width) of a grouped call."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError(f"{name} must be a stack of matrices [E_loc, cols, inner]")
+    n, N, K = w.shape
+    _int32(N, K)
+    _need(offsets, "offsets", torch.int32, (n + 1,))
+    _need(counts, "counts", torch.int32, (n,))
+    _same_device(rows.device, offsets, counts, w)
+    return GroupedFp8Desc(m_cap, m_cap if max_rows is None else max_rows, 0, n, K, N, 0), n, K, N
+
+
+def grouped_gate_up_fp8(x: torch.Tensor, x_scale: torch.Tensor, offsets, counts, w1, w1_scale, w3,
+                        w3_scale, src_row=None, top_k: int = 1, max_rows=None, h=None,
+                        h_scale=None):
+    """(h [m_cap, I] e4m3, h_scale [m_cap, I / 128] fp32) = silu(x W1) * (x W3) per local
+    expert group, on 8-bit rows x [m_cap, H] with x_scale [m_cap, H / 128] or, with
+    ``src_row``, on token rows [T, H], grouped row r being x[src_row[r] // top_k].
+    w1, w3 [E_loc, I, H] e4m3 with scales [E_loc, I / 128, H / 128] (quantize_fp8_weights
+    with ``transpose`` of the math orientation). Rows of a group past ``max_rows`` (the
+    token count, say) are not computed; rows outside the groups not written."""
+    dev = x.device
+    gather = src_row is not None
+    if gather:
+        _need(src_row, "src_row", torch.int32, (src_row.numel(),))
+    rows = x.shape[0]
+    m_cap = src_row.numel() if gather else rows
+    desc, n, H, I = _grouped_fp8(x, offsets, counts, w1, m_cap, max_rows, "w1")
+    if gather:
+        desc.num_tokens, desc.top_k = rows, top_k
+    _need_fp8(x, x_scale, "x", (rows, H), (rows, _runs(H)))
+    for w, s, name in ((w1, w1_scale, "w1"), (w3, w3_scale, "w3")):
+        _need_fp8(w, s, name, (n, I, H), (n, _runs(I), _runs(H)))
+    h = _out(h, "h", _F8, (m_cap, I), dev)
+    h_scale = _out(h_scale, "h_scale", torch.float32, (m_cap, _runs(I)), dev)
+    _same_device(dev, x_scale, src_row, w1_scale, w3, w3_scale)
+    _run(dev, "moe_grouped_gate_up_fp8", C.byref(desc), x.data_ptr(), x_scale.data_ptr(),
+         _at(src_row), offsets.data_ptr(), counts.data_ptr(), w1.data_ptr(), w1_scale.data_ptr(),
+         w3.data_ptr(), w3_scale.data_ptr(), h.data_ptr(), h_scale.data_ptr())
+    return h, h_scale
+
+
+def grouped_down_fp8(h: torch.Tensor, h_scale: torch.Tensor, offsets, counts, w2, w2_scale,
+                     max_rows=None, out=None) -> torch.Tensor:
+    """y [m_cap, H] bf16 = h W2 per local expert group, on 8-bit h [m_cap, I] with h_scale
+    [m_cap, I / 128] and w2 [E_loc, H, I] with w2_scale [E_loc, H / 128, I / 128];
+    ``max_rows`` as in grouped_gate_up_fp8."""
+    dev = h.device
+    m_cap = h.shape[0]
+    desc, n, I, H = _grouped_fp8(h, offsets, counts, w2, m_cap, max_rows, "w2")
+    _need_fp8(h, h_scale, "h", (m_cap, I), (m_cap, _runs(I)))
+    _need_fp8(w2, w2_scale, "w2", (n, H, I), (n, _runs(H), _runs(I)))
+    out = _out(out, "y", torch.bfloat16, (m_cap, H), dev)
+    _same_device(dev, h_scale, w2_scale)
+    _run(dev, "moe_grouped_down_fp8", C.byref(desc), h.data_ptr(), h_scale.data_ptr(),
+         offsets.data_ptr(), counts.data_ptr(), w2.data_ptr(), w2_scale.data_ptr(), out.data_ptr())
+    return out
 
 
 # ---------------------------------------------------------------- combine

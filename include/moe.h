@@ -623,6 +623,93 @@ int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mat
                                  void* stream);
 
 /*
+ * moe_linear_fp8 -- moe_linear on 8-bit operands.
+ *
+ *   z[m, n] = sum over runs b of x_scale[m, b] w_scale[n / 128, b] (sum over k in run b of x[m, k] w[n, k])
+ *             + bias[n]
+ *   y = act(z) + residual      fp32, rounded once to y's type
+ *
+ * The products of a run are summed on the matrix cores, the runs in fp32. act as in moe_linear.
+ * The gradient of x is the same product with the transposed weights: blocks of 128 x 128
+ * keep their values when turned over (moe_quantize_fp8_weights with the other w_order).
+ *   x_d         [rows, inner] e4m3, dense;  x_scale_d [rows, ceil(inner / 128)] float
+ *   w_d         [cols, inner] e4m3, dense;  w_scale_d [ceil(cols / 128), ceil(inner / 128)] float
+ *   bias_d      [cols] float, or NULL
+ *   residual_d  [rows, cols] of `dtype`, row stride ldr, or NULL
+ *   y_d         [rows, cols] of `dtype` or (y_f32) float, row stride ldy (out)
+ * y may be the residual itself (same address, stride and type); other buffers must not overlap.
+ * Limits: 0 <= rows < 2^31, inner a multiple of 16 from 16 to 2^20, 1 <= cols <= 2^20; dtype
+ * MOE_ROWS_BF16 or MOE_ROWS_F16; ldy and (read only with its buffer) ldr from cols to 2^21; fewer than 2^26
+ * tiles of 128 x 128 outputs and 2^35 outputs (else MOE_ERR_UNSUPPORTED). x_d and w_d 16-byte aligned.
+ *   workspace_d >= moe_linear_fp8_workspace_bytes(desc) bytes, 16-byte aligned (NULL if that
+ *   is 0); contents on entry do not matter. Calls that may overlap need workspaces of their own.
+ */
+typedef struct moe_linear_fp8_desc {
+  int64_t rows;  /* M */
+  int32_t inner; /* K */
+  int32_t cols;  /* N */
+  int32_t dtype; /* MOE_ROWS_BF16 or MOE_ROWS_F16: of y (unless y_f32) and the residual */
+  int32_t act;   /* MOE_ACT_* */
+  int32_t y_f32; /* 0 or 1 */
+  int32_t reserved; /* 0 */
+  int64_t ldy, ldr;
+} moe_linear_fp8_desc;
+
+size_t moe_linear_fp8_workspace_bytes(const moe_linear_fp8_desc* desc);
+
+int32_t moe_linear_fp8(const moe_linear_fp8_desc* desc, const void* x_d, const float* x_scale_d,
+                       const void* w_d, const float* w_scale_d, const float* bias_d,
+                       const void* residual_d, void* y_d, void* workspace_d,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Grouped SwiGLU expert MLPs on 8-bit operands: moe_grouped_gate_up (and, with src_row_d,
+ * moe_grouped_gate_up_gather) and moe_grouped_down with e4m3 rows, e4m3 weights and their scales,
+ * for serving. For local expert e the rows [offsets[e], offsets[e] + counts[e]):
+ *
+ *   moe_grouped_gate_up_fp8:  h = silu(x W1[e]) * (x W3[e]), fp32, then e4m3 with a scale for each
+ *                             128 columns of a row, as moe_quantize_fp8 takes it
+ *   moe_grouped_down_fp8:     y = h W2[e], rounded once to bf16
+ *
+ * sums as in moe_linear_fp8. Rows outside the groups are neither read nor written.
+ *   x_d        [m_cap, inner] e4m3, or with src_row_d [num_tokens, inner]: row r of the groups is then
+ *              x[src_row[r] / top_k] (moe_layout's src_row); a row whose src_row is not of [0, num_tokens top_k)
+ *              holds no defined values
+ *   x_scale_d  [rows of x, inner / 128] float
+ *   w1_d, w3_d, w2_d  [num_groups, cols, inner] e4m3, output-major (moe_quantize_fp8_weights with MOE_W_KN
+ *              takes the math orientation); their scales [num_groups, cols / 128, inner / 128] float
+ *   offsets_d  [num_groups + 1], counts_d [num_groups] int32, as in moe_grouped_gate_up
+ *   h_d        [m_cap, cols] e4m3, h_scale_d [m_cap, cols / 128] float (out);  y_d [m_cap, cols] bf16 (out)
+ *   max_rows   a group's rows from max_rows on are not computed (the token count, say: a token
+ *              comes to an expert once)
+ * gate_up: inner is the hidden size, cols the experts' inner size; down: the other way round.
+ * Limits: inner and cols multiples of 128, at most 2^20; 1 <= num_groups <= 1024; m_cap < 2^31; with
+ * src_row_d 1 <= top_k <= 16 and num_tokens * inner < 2^31; m_cap / 65 + num_groups tiles of 256 columns (gate_up:
+ * 128) fewer than 2^30; else MOE_ERR_UNSUPPORTED. Device pointers 16-byte aligned (offsets_d, counts_d, src_row_d: 4).
+ */
+typedef struct moe_grouped_fp8_desc {
+  int64_t m_cap;
+  int64_t max_rows;
+  int64_t num_tokens; /* with src_row_d */
+  int32_t num_groups;
+  int32_t inner;
+  int32_t cols;
+  int32_t top_k; /* with src_row_d */
+} moe_grouped_fp8_desc;
+
+int32_t moe_grouped_gate_up_fp8(const moe_grouped_fp8_desc* desc, const void* x_d,
+                                const float* x_scale_d, const int32_t* src_row_d,
+                                const int32_t* offsets_d, const int32_t* counts_d,
+                                const void* w1_d, const float* w1_scale_d, const void* w3_d,
+                                const float* w3_scale_d, void* h_d, float* h_scale_d,
+                                void* stream);
+
+int32_t moe_grouped_down_fp8(const moe_grouped_fp8_desc* desc, const void* h_d,
+                             const float* h_scale_d, const int32_t* offsets_d,
+                             const int32_t* counts_d, const void* w2_d, const float* w2_scale_d,
+                             void* y_d, void* stream);
+
+/*
  * moe_combine -- fused weighted-sum restore.
  *
  * The fused restore of DeepSpeed PR #8847 ("AutoEP: support

@@ -187,3 +187,100 @@ def test_quantize_argument_checks_launch_nothing():
                        (dict(s=x), 1), (dict(s=q), 1)):
         assert weights(**kw) == status, kw
     assert weights(n=0, w=None, q=None, s=None) == 0
+
+
+def _linear_desc(**kw):
+    from combine_top_router_amd._lib import LinearFp8Desc
+    d = dict(rows=4, inner=128, cols=64, dtype=0, act=0, y_f32=0, reserved=0, ldy=64, ldr=64)
+    d.update(kw)
+    return LinearFp8Desc(*(d[k] for k, _ in LinearFp8Desc._fields_))
+
+
+@built
+@pytest.mark.parametrize("bad, status", [
+    (dict(rows=-1), 1), (dict(rows=1 << 31), 1), (dict(inner=0), 1), (dict(inner=(1 << 20) + 16), 1),
+    (dict(cols=0), 1), (dict(cols=(1 << 20) + 1), 1), (dict(act=4), 1), (dict(act=-1), 1),
+    (dict(y_f32=2), 1), (dict(reserved=1), 1), (dict(ldy=63), 1), (dict(ldy=(1 << 21) + 1), 1),
+    (dict(dtype=2), 2), (dict(inner=24), 2), (dict(rows=1 << 24, cols=1 << 20, ldy=1 << 20), 2),
+    (dict(rows=(1 << 31) - 1, cols=128, ldy=128), 2),
+])
+def test_bad_linear_fp8_descriptors_are_refused(bad, status):
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    d = _linear_desc(**bad)
+    f = [C.c_void_p((i + 1) << 20) for i in range(8)]  # never dereferenced
+    assert lib.moe_linear_fp8_workspace_bytes(C.byref(d)) == 0
+    assert lib.moe_linear_fp8(C.byref(d), *f, 1 << 40, None) == status
+
+
+@built
+def test_linear_fp8_argument_checks_launch_nothing():
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    names = ("x", "xs", "w", "ws", "bias", "res", "y", "work")
+    at = {n: C.c_void_p((i + 1) << 20) for i, n in enumerate(names)}
+    odd = C.c_void_p((20 << 20) + 8)
+
+    def call(d=None, n=1 << 40, **kw):
+        a = dict(at, **kw)
+        return lib.moe_linear_fp8(C.byref(d or _linear_desc()), *(a[k] for k in names), n, None)
+
+    assert lib.moe_linear_fp8(None, *at.values(), 1 << 40, None) == 1
+    for kw in (dict(x=None), dict(xs=None), dict(w=None), dict(ws=None), dict(y=None), dict(x=odd),
+               dict(w=odd), dict(y=at["res"], d=_linear_desc(ldr=72)),
+               dict(y=at["res"], d=_linear_desc(y_f32=1)), dict(d=_linear_desc(ldr=63))):
+        assert call(**kw) == 1, kw
+    for n in ("x", "xs", "w", "ws", "bias"):
+        assert call(y=at[n]) == 1, n
+    assert call(d=_linear_desc(rows=0), x=None, w=None, y=None) == 0
+    split = _linear_desc(rows=100, inner=8192, cols=128, ldy=128, ldr=128)
+    need = lib.moe_linear_fp8_workspace_bytes(C.byref(split))
+    assert need > 0
+    assert call(d=split, work=None) == 1 and call(d=split, n=need - 1) == 1 and call(d=split, work=odd) == 1
+
+
+def _grouped_desc(**kw):
+    from combine_top_router_amd._lib import GroupedFp8Desc
+    d = dict(m_cap=256, max_rows=256, num_tokens=64, num_groups=2, inner=128, cols=128, top_k=2)
+    d.update(kw)
+    return GroupedFp8Desc(*(d[k] for k, _ in GroupedFp8Desc._fields_))
+
+
+@built
+def test_grouped_fp8_argument_checks_launch_nothing():
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    up = ("x", "xs", "src", "off", "cnt", "w1", "s1", "w3", "s3", "h", "hs")
+    down = ("h", "hs", "off", "cnt", "w2", "s2", "y")
+    odd = C.c_void_p((20 << 20) + 8)
+
+    def call(fn, names, d=None, **kw):
+        a = dict({n: C.c_void_p((i + 1) << 20) for i, n in enumerate(names)}, **kw)
+        return fn(C.byref(d or _grouped_desc()), *(a[k] for k in names), None)
+
+    for fn, names in ((lib.moe_grouped_gate_up_fp8, up), (lib.moe_grouped_down_fp8, down)):
+        for bad, status in ((dict(m_cap=-1), 1), (dict(max_rows=-1), 1), (dict(num_groups=0), 1),
+                            (dict(num_groups=1025), 1), (dict(inner=0), 1), (dict(cols=0), 1),
+                            (dict(inner=(1 << 20) + 128), 1), (dict(cols=(1 << 20) + 128), 1),
+                            (dict(inner=192), 2), (dict(cols=192), 2), (dict(m_cap=1 << 31), 2),
+                            (dict(m_cap=(1 << 31) - 1, cols=1 << 20), 2)):
+            assert call(fn, names, _grouped_desc(**bad)) == status, (fn, bad)
+        assert fn(None, *[C.c_void_p(1 << 20)] * len(names), None) == 1
+        for n in names:
+            if n != "src":
+                assert call(fn, names, **{n: None}) == 1, n
+            if n not in ("src", "off", "cnt"):
+                assert call(fn, names, **{n: odd}) == 1, n
+        assert call(fn, names, _grouped_desc(m_cap=0)) == 0
+        assert call(fn, names, _grouped_desc(max_rows=0)) == 0
+    a = {n: C.c_void_p((i + 1) << 20) for i, n in enumerate(up)}
+    for n in ("x", "xs", "w1", "s1", "w3", "s3"):
+        assert call(lib.moe_grouped_gate_up_fp8, up, h=a[n]) == 1, n
+        assert call(lib.moe_grouped_gate_up_fp8, up, hs=a[n]) == 1, n
+    for bad, status in ((dict(top_k=0), 1), (dict(top_k=17), 1), (dict(num_tokens=-1), 1),
+                        (dict(num_tokens=1 << 24), 2)):
+        assert call(lib.moe_grouped_gate_up_fp8, up, _grouped_desc(**bad)) == status, bad
+    assert call(lib.moe_grouped_gate_up_fp8, up, _grouped_desc(num_tokens=0)) == 0
+    b = {n: C.c_void_p((i + 1) << 20) for i, n in enumerate(down)}
+    for n in ("h", "hs", "w2", "s2"):
+        assert call(lib.moe_grouped_down_fp8, down, y=b[n]) == 1, n
