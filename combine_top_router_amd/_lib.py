@@ -56,7 +56,7 @@ class LinearFp8Desc(C.Structure):
 class GroupedFp8Desc(C.Structure):
     _fields_ = [("m_cap", C.c_int64), ("max_rows", C.c_int64), ("num_tokens", C.c_int64),
                 ("num_groups", C.c_int32), ("inner", C.c_int32), ("cols", C.c_int32),
-                ("top_k", C.c_int32)]
+                ("top_k", C.c_int32), ("fast", C.c_int32), ("reserved", C.c_int32)]
 
 
 _P = C.c_void_p

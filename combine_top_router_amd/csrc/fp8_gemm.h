@@ -17,7 +17,6 @@ constexpr int kWaves8 = 8;
 constexpr int kThreads8 = 64 * kWaves8;
 constexpr uint32_t kPast = 0x80000000u;  // a byte offset past every buffer range
 constexpr int kBandRows = 4;             // row tiles walked together
-constexpr int kDirectRows = 64;          // ragged: a group of so many rows is read straight into registers
 
 // kDense    one group of M rows, c through the linear layer's epilogue
 // kGrouped  ragged groups, each with a matrix of its own; c as kDense
@@ -49,9 +48,15 @@ struct Fp8Args {
   float* hs;               // [rows, N / 128]
 };
 
-// 4 bytes per lane, memory -> LDS, as dma16; four more wait states, for an offset that the
-// compiler restores from a spill right before it.
-__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
+// 16 and 4 bytes per lane, memory -> LDS, as dma16, with four more wait states: this kernel has
+// places where the compiler restores a scalar operand from a spill right before the
+// transfer. They pass while the matrix cores are busy with the product before.
+__device__ __forceinline__ void load16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
+               "{m0}"(lds_addr)
+               : "memory");
+}
+__device__ __forceinline__ void load4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds_addr) {
   asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff),
                "{m0}"(lds_addr)
                : "memory");
@@ -77,7 +82,8 @@ __device__ __forceinline__ f16v8 to_f16(int lo, int hi) {
 // of 2^-13 of the largest one's power of two (measured; the eights and the runs are added with 24
 // bits): 1.4e-5 of the result's norm on normal values, unbiased, far below an output of
 // 16 or 8 bits. EXACT goes through fp16, which holds every e4m3 value, at half the rate: its
-// sums keep 24 bits throughout (2e-7 a run). Taken for fp32 outputs, and where reading w is the bound.
+// sums keep 24 bits throughout (2e-7 a run). Taken for fp32 outputs (gate/up's scales are some), and
+// where reading w is the bound.
 template <bool EXACT>
 __device__ __forceinline__ f32x4 run_product(const i32x8& w, const i32x8& a) {
   if constexpr (EXACT) {
@@ -102,6 +108,15 @@ __device__ __forceinline__ float silu8(float g) {
 constexpr int block_of(int p, int nb) { return p < (nb - 2) * 4 ? p / 4 : nb - 2 + ((p - (nb - 2) * 4) & 1); }
 constexpr int column_of(int p, int nb) { return p < (nb - 2) * 4 ? p % 4 : (p - (nb - 2) * 4) / 2; }
 
+// f(nb) at compile time, for nb from 2 (taken for fewer) to MB.
+template <int MB, class F>
+__device__ __forceinline__ void with_blocks(int nb, F&& f) {
+  if constexpr (MB > 2) {
+    if (nb < MB) return with_blocks<MB - 1>(nb, f);
+  }
+  f(std::integral_constant<int, MB>{});
+}
+
 // WIDE: rows of the outputs go out in 16-byte pieces (always so for the ragged kinds).
 // EXACT: run_product's
 template <int BM, int BN, int NS, int KIND, bool WIDE, bool EXACT>
@@ -109,16 +124,16 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
   constexpr bool GATED = KIND == kGated, RAGGED = KIND != kDense;
   constexpr int WN = BN / 64, WM = kWaves8 / WN, MB = BM / WM / 16;  // a wavefront: 16 MB rows x 64 staged columns
   constexpr int OUT = GATED ? BN / 2 : BN;  // output columns of a tile
-  constexpr int A_BYTES = BM * kRun, B_BYTES = BN * kRun, S_BYTES = kThreads8 * 4;
+  constexpr int A_BYTES = (BM + 63) / 64 * 64 * kRun, B_BYTES = BN * kRun, S_BYTES = kThreads8 * 4;
   constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
-  constexpr int AL = BM / 64, BL = BN / 64, NL = AL + BL + 1;  // wave-loads of a slice
-  constexpr int SW = BM / 64;  // the wavefront that brings w's scales; those before it bring the rows'
-  static_assert(MB >= 2 && MB % 2 == 0 && WM * WN == kWaves8 && SW + 1 < kWaves8, "tile");
+  constexpr int AL = (BM + 63) / 64, BL = BN / 64, NL = AL + BL + 1;  // wave-loads of a slice
+  constexpr int MS = (MB + 1) / 2 * 2;   // places of a row's scales in a stage
+  constexpr int SW = (WM * 16 * MS + 63) / 64;  // the wavefront that brings w's scales; those before it bring the rows'
+  static_assert(MB >= 2 && WM * WN == kWaves8 && SW + 1 < kWaves8, "tile");
   __shared__ __attribute__((aligned(1024))) char smem[NS * STAGE];
-  // of each group: its rows, its first row, and the row tiles of the groups before it,
-  // those of more than kDirectRows rows in [0], the others' in [1]
-  __shared__ int mt_prefix[2][RAGGED ? kMaxGroups + 1 : 1], cnt_s[RAGGED ? kMaxGroups : 1],
-      off_s[RAGGED ? kMaxGroups : 1], wave_tot[2][kWaves8];
+  // of each group: the row tiles before it, its rows, its first row
+  __shared__ int mt_prefix[RAGGED ? kMaxGroups + 1 : 1], cnt_s[RAGGED ? kMaxGroups : 1],
+      off_s[RAGGED ? kMaxGroups : 1], wave_tot[kWaves8];
   __shared__ uint32_t amax_s[GATED ? WN * BM : 1];
 
   const int tid = threadIdx.x, lane = lane_id(), wid = uniform(tid / kWave);
@@ -127,11 +142,11 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
   const int K = g.K, N = g.N, KT = g.runs;
   const int NT = (N + OUT - 1) / OUT;
 
-  int total, with_few = 0;  // tiles, and those with the groups of few rows behind them
+  int total;
   if constexpr (RAGGED) {
     // a group's rows stay inside [0, m_cap) whatever the device's counts say
     constexpr int PER = kMaxGroups / kThreads8;
-    int v[2][PER], run[2] = {0, 0}, incl[2];
+    int v[PER], run = 0;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int e = tid * PER + q;
@@ -142,36 +157,28 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
         c = int(min(int64_t(min(max(g.counts[e], 0), g.max_rows)), room));
         cnt_s[e] = c, off_s[e] = o;
       }
-      v[0][q] = c > kDirectRows ? (c + BM - 1) / BM : 0;
-      v[1][q] = c > 0 && c <= kDirectRows ? 1 : 0;
-      run[0] += v[0][q], run[1] += v[1][q];
+      v[q] = (c + BM - 1) / BM;
+      run += v[q];
     }
+    int incl = run;
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      incl[z] = run[z];
-#pragma unroll
-      for (int off = 1; off < kWave; off <<= 1) {
-        const int o = __shfl_up(incl[z], off, kWave);
-        if (lane >= off) incl[z] += o;
-      }
-      if (lane == kWave - 1) wave_tot[z][wid] = incl[z];
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int o = __shfl_up(incl, off, kWave);
+      if (lane >= off) incl += o;
     }
+    if (lane == kWave - 1) wave_tot[wid] = incl;
     __syncthreads();
+    int ex = incl - run;
+    for (int w = 0; w < wid; ++w) ex += wave_tot[w];
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      int ex = incl[z] - run[z];
-      for (int w = 0; w < wid; ++w) ex += wave_tot[z][w];
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const int e = tid * PER + q;
-        if (e < g.groups) mt_prefix[z][e] = ex;
-        ex += v[z][q];
-      }
-      if (tid == kThreads8 - 1) mt_prefix[z][g.groups] = ex;
+    for (int q = 0; q < PER; ++q) {
+      const int e = tid * PER + q;
+      if (e < g.groups) mt_prefix[e] = ex;
+      ex += v[q];
     }
+    if (tid == kThreads8 - 1) mt_prefix[g.groups] = ex;
     __syncthreads();
-    total = uniform(mt_prefix[0][g.groups]) * NT;
-    with_few = total + uniform(mt_prefix[1][g.groups]) * NT;
+    total = uniform(mt_prefix[g.groups]) * NT;
   } else {
     total = g.tiles_m * NT * g.splits;
   }
@@ -187,20 +194,19 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
   // Tile ids run group by group, inside a group in bands of kBandRows row tiles, column tile
   // major inside a band: the 32 neighbours of an XCD share the rows of 4 row tiles
   // and the columns of 8 column tiles behind one L2.
-  auto locate = [&](int id, auto few) {
+  auto locate = [&](int id) {
     Tile t;
     int mtiles, rem, rows;
     if constexpr (RAGGED) {
-      const int* before = mt_prefix[decltype(few)::value];
       int lo = 0, hi = g.groups - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (before[mid] * NT <= id) lo = mid; else hi = mid - 1;
+        if (mt_prefix[mid] * NT <= id) lo = mid; else hi = mid - 1;
       }
       t.e = uniform(lo);
       t.split = 0;
-      mtiles = uniform(before[t.e + 1] - before[t.e]);
-      rem = id - uniform(before[t.e]) * NT;
+      mtiles = uniform(mt_prefix[t.e + 1] - mt_prefix[t.e]);
+      rem = id - uniform(mt_prefix[t.e]) * NT;
       rows = uniform(cnt_s[t.e]);
     } else {
       const int tiles = g.tiles_m * NT;
@@ -278,8 +284,8 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     // each other; SW those of w (two runs of columns, or w0's) and, gated, SW + 1 those of w1
     osc = kPast;
     if (wid < SW) {
-      const int s = wid * 64 + lane, w = s / MB;
-      const int r = source(((s % MB) * WM + w / 16) * 16 + (w & 15));
+      const int s = wid * 64 + lane, w = s / MS;
+      const int r = s % MS < MB ? source(((s % MS) * WM + w / 16) * 16 + (w & 15)) : -1;
       if (r >= 0) osc = uint32_t(r) * uint32_t(KT) * 4u;
       rsc = make_rsrc(g.sa + a0 * KT, a_rows * uint32_t(KT) * 4u);
     } else {
@@ -298,13 +304,13 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     if constexpr (q >= NL) {
       return;
     } else if constexpr (q < BL) {
-      dma16(GATED && q >= BL / 2 ? rb1 : rb0, b_ch * 16 < left ? ob[q] : kPast, uint32_t(kt) * kRun,
+      load16(GATED && q >= BL / 2 ? rb1 : rb0, b_ch * 16 < left ? ob[q] : kPast, uint32_t(kt) * kRun,
             at + A_BYTES + (wid + kWaves8 * q) * 1024);
     } else if constexpr (q < BL + AL) {
-      dma16(ra, a_ch * 16 < left ? oa[q - BL] : kPast, uint32_t(kt) * kRun,
+      load16(ra, a_ch * 16 < left ? oa[q - BL] : kPast, uint32_t(kt) * kRun,
             at + (wid + kWaves8 * (q - BL)) * 1024);
     } else {
-      dma4(rsc, left > 0 ? osc : kPast, uint32_t(kt) * 4u, at + A_BYTES + B_BYTES + wid * 256);
+      load4(rsc, left > 0 ? osc : kPast, uint32_t(kt) * 4u, at + A_BYTES + B_BYTES + wid * 256);
     }
   };
   auto first_slices = [&](int k0, int k1) {
@@ -329,8 +335,8 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     int at_b = A_BYTES + (8 * (r15 >> 2) + (r15 & 3)) * kRun +
                ((grp ^ (((r15 >> 1) & 1) | ((r15 >> 2) << 1))) << 4);
     int at_a2 = at_a ^ 64, at_b2 = at_b ^ 64;
-    int at_s = A_BYTES + B_BYTES + (wm * 16 + r15) * (MB * 4);
-    int at_w = A_BYTES + B_BYTES + BM * 4 + (GATED ? 0 : wn * 64 / kRun * 4);
+    int at_s = A_BYTES + B_BYTES + (wm * 16 + r15) * (MS * 4);
+    int at_w = A_BYTES + B_BYTES + SW * 256 + (GATED ? 0 : wn * 64 / kRun * 4);
     asm volatile("" : "+v"(at_a), "+v"(at_b), "+v"(at_a2), "+v"(at_b2), "+v"(at_s));
     auto read_a = [&](int i, int to) __attribute__((always_inline)) {
       const int o = (i * WM + wm) * (16 * kRun);
@@ -539,117 +545,6 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     }
   };
 
-  // A tile of few rows is bound by reading w, once: its wavefronts take 32 of the
-  // tile's w rows each and read them straight into registers, D runs ahead, with no barrier.
-  // RB: blocks of 16 rows.
-  auto direct = [&](const Tile& t, auto rb_tag, auto d_tag) {
-    constexpr int RB = decltype(rb_tag)::value, D = decltype(d_tag)::value;
-    const uint8_t *pw[2], *pa[RB];
-    const float* psa[RB];
-    const int nblocks = (N + kRun - 1) / kRun;
-    // plain: columns 32 wid + 8 grp .. + 7 in a lane; gated: gate and up columns 16 wid + 4 grp .. + 3
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = GATED ? wid * 16 + r15 : wid * 32 + 8 * (r15 >> 2) + (r15 & 3) + 4 * j;
-      const uint8_t* w = GATED && j ? g.w1 : g.w0;
-      pw[j] = w + (int64_t(t.e) * N + min(t.n0 + n, N - 1)) * K + grp * 16;
-    }
-    const int wb = min(t.n0 / kRun + (GATED ? 0 : wid * 32 / kRun), nblocks - 1);
-    const float* ps0 = g.s0 + (int64_t(t.e) * nblocks + wb) * KT;
-    const float* ps1 = GATED ? g.s1 + (int64_t(t.e) * nblocks + wb) * KT : ps0;
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      // (rows past the tile's: the last one again; a row of a reaches its own outputs alone)
-      int64_t r = t.row0 + min(i * 16 + r15, t.rows - 1);
-      if (GATED && g.gather) {
-        const int src = g.gather[r];
-        r = src >= 0 ? min(int64_t(src / g.top_k), g.tokens - 1) : 0;
-      }
-      pa[i] = g.a + r * K + grp * 16;
-      psa[i] = g.sa + r * KT;
-    }
-    f32x4 sum[RB][2];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) sum[i][0] = sum[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    struct Run {
-      u32x4 w[2][2], a[RB][2];
-      float sa[RB], s0, s1;
-    } ring[D];
-    auto fetch = [&](Run& x, int kt) __attribute__((always_inline)) {
-      const int k = min(kt, KT - 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int z = 0; z < 2; ++z) x.w[j][z] = *reinterpret_cast<const u32x4*>(pw[j] + k * kRun + z * 64);
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-#pragma unroll
-        for (int z = 0; z < 2; ++z) x.a[i][z] = *reinterpret_cast<const u32x4*>(pa[i] + k * kRun + z * 64);
-        x.sa[i] = psa[i][k];
-      }
-      x.s0 = ps0[k];
-      if constexpr (GATED) x.s1 = ps1[k];
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) fetch(ring[d], d);
-    for (int kt = 0; kt < KT; kt += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        Run& x = ring[d];
-        if (kt + d < KT) {
-#pragma unroll
-          for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const f32x4 p = run_product<true>(join(x.w[j][0], x.w[j][1]), join(x.a[i][0], x.a[i][1]));
-              const float s = x.sa[i] * (GATED && j ? x.s1 : x.s0);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) sum[i][j][q] = __builtin_fmaf(p[q], s, sum[i][j][q]);
-            }
-        }
-        fetch(x, kt + d + D);
-      }
-    }
-    if constexpr (GATED) {
-      float hv[RB][4];
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) hv[i][q] = silu8(sum[i][0][q]) * sum[i][1][q];
-        const uint32_t m = amax_row(magnitude(hv[i]));
-        if (grp == 0) amax_s[wid * (16 * RB) + i * 16 + r15] = m;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const int r = i * 16 + r15;
-        if (r >= t.rows) continue;
-        uint32_t m = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves8; ++w) m = max(m, amax_s[w * (16 * RB) + r]);
-        const float s = scale_of(m);
-        const int64_t row = t.row0 + r;
-        const float v[8] = {hv[i][0], hv[i][1], hv[i][2], hv[i][3], 0.f, 0.f, 0.f, 0.f};
-        *reinterpret_cast<uint32_t*>(g.h + row * N + t.n0 + wid * 16 + grp * 4) = to_fp8x8(v, 1.f / s).x;
-        if (wid == 0 && grp == 0) g.hs[row * (N / kRun) + t.n0 / kRun] = s;
-      }
-    } else {
-      const int64_t nw = t.n0 + wid * 32;
-      const Block b(g.e, t.row0, nw);
-      float bias[8];
-      column_bias(nw + grp * 8, bias);
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const int r = i * 16 + r15;
-        if (r >= t.rows || nw + grp * 8 >= N) continue;
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = sum[i][q >> 2][q & 3];
-        finish8(g.e, b, r, grp * 8, v, bias, u32x4{0, 0, 0, 0});
-      }
-    }
-  };
-
   // ---- the tiles
   auto range = [&](const Tile& t, int& k0, int& k1) {
     k0 = KIND == kDense ? t.split * g.per_split : 0;
@@ -663,7 +558,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
   };
   int id = slot;
   if (id < total) {
-    Tile t = locate(id, std::integral_constant<int, 0>{});
+    Tile t = locate(id);
     begin(t);
     for (;;) {
       int k0, k1;
@@ -673,10 +568,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       const int nb = ((t.rows + 15) / 16 + WM - 1) / WM;  // row blocks of a wavefront
-      constexpr int B4 = MB >= 8 ? MB - 4 : 2, B2 = MB >= 4 ? MB - 2 : 2;
-      if (MB >= 8 && nb <= B4) kloop(std::integral_constant<int, B4>{}, k0, k1);
-      else if (MB >= 4 && nb <= B2) kloop(std::integral_constant<int, B2>{}, k0, k1);
-      else kloop(std::integral_constant<int, MB>{}, k0, k1);
+      with_blocks<MB>(nb, [&](auto b) __attribute__((always_inline)) { kloop(b, k0, k1); });
       wait_vmcnt<0>();
       __syncthreads();  // the stages are free
       id += G;
@@ -685,7 +577,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
         break;
       }
       const Tile now = t;
-      t = locate(id, std::integral_constant<int, 0>{});
+      t = locate(id);
       if constexpr (WIDE) {
         begin(t);  // the next tile's first slices are on their way during this one's epilogue
         epilogue(now);
@@ -694,15 +586,6 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
         __syncthreads();  // LDS is read out before it is written again
         begin(t);
       }
-    }
-  }
-  if constexpr (RAGGED) {
-    for (; id < with_few; id += G) {
-      __syncthreads();  // amax_s is read out
-      const Tile t = locate(id - total, std::integral_constant<int, 1>{});
-      if (t.rows <= 16) direct(t, std::integral_constant<int, 1>{}, std::integral_constant<int, 6>{});
-      else if (t.rows <= 32) direct(t, std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
-      else direct(t, std::integral_constant<int, 4>{}, std::integral_constant<int, 3>{});
     }
   }
 }

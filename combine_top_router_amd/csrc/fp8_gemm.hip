@@ -230,7 +230,8 @@ hipError_t launch_gate_up_fp8(const moe_grouped_fp8_desc& d, const void* x, cons
   g.m_cap = d.m_cap, g.max_rows = static_cast<int>(std::min<int64_t>(d.max_rows, INT32_MAX));
   g.gather = src_row, g.top_k = d.top_k, g.tokens = d.num_tokens;
   g.h = static_cast<uint8_t*>(h), g.hs = hs;
-  return launch8<kGated, 256, 256, 2>(g, INT64_MAX, s);
+  if (d.fast) return launch8<kGated, 256, 256, 2>(g, INT64_MAX, s);
+  return launch8<kGated, 192, 256, 2, true>(g, INT64_MAX, s);
 }
 
 hipError_t launch_down_fp8(const moe_grouped_fp8_desc& d, const void* h, const float* hs,

@@ -728,7 +728,8 @@ int32_t moe_linear_fp8(const moe_linear_fp8_desc* desc, const void* x_d, const f
 static int32_t grouped_fp8_status(const moe_grouped_fp8_desc* d, bool gather, int tile) {
   constexpr int32_t kDim = 1 << 20;
   if (!d || d->m_cap < 0 || d->max_rows < 0 || d->num_groups < 1 || d->num_groups > kMaxExperts ||
-      d->inner < 1 || d->inner > kDim || d->cols < 1 || d->cols > kDim)
+      d->inner < 1 || d->inner > kDim || d->cols < 1 || d->cols > kDim || (d->fast != 0 && d->fast != 1) ||
+      d->reserved)
     return MOE_ERR_ARG;
   if (gather && (d->num_tokens < 0 || d->top_k < 1 || d->top_k > kMaxTopK)) return MOE_ERR_ARG;
   if (d->inner % 128 || d->cols % 128 || d->m_cap >= (int64_t(1) << 31) ||

@@ -718,18 +718,20 @@ def _grouped_fp8(rows, offsets, counts, w, m_cap: int, max_rows, name: str):
     _need(offsets, "offsets", torch.int32, (n + 1,))
     _need(counts, "counts", torch.int32, (n,))
     _same_device(rows.device, offsets, counts, w)
-    return GroupedFp8Desc(m_cap, m_cap if max_rows is None else max_rows, 0, n, K, N, 0), n, K, N
+    return GroupedFp8Desc(m_cap, m_cap if max_rows is None else max_rows, 0, n, K, N, 0, 0, 0), n, K, N
 
 
 def grouped_gate_up_fp8(x: torch.Tensor, x_scale: torch.Tensor, offsets, counts, w1, w1_scale, w3,
                         w3_scale, src_row=None, top_k: int = 1, max_rows=None, h=None,
-                        h_scale=None):
+                        h_scale=None, fast: bool = False):
     """(h [m_cap, I] e4m3, h_scale [m_cap, I / 128] fp32) = silu(x W1) * (x W3) per local
     expert group, on 8-bit rows x [m_cap, H] with x_scale [m_cap, H / 128] or, with
     ``src_row``, on token rows [T, H], grouped row r being x[src_row[r] // top_k].
     w1, w3 [E_loc, I, H] e4m3 with scales [E_loc, I / 128, H / 128] (quantize_fp8_weights
     with ``transpose`` of the math orientation). Rows of a group past ``max_rows`` (the
-    token count, say) are not computed; rows outside the groups not written."""
+    token count, say) are not computed; rows outside the groups not written. ``fast``: sums by
+    the 8-bit matrix instruction, up to 1.8 times as fast with many rows to a group, the
+    scales 1.2e-5 off."""
     dev = x.device
     gather = src_row is not None
     if gather:
@@ -739,6 +741,7 @@ def grouped_gate_up_fp8(x: torch.Tensor, x_scale: torch.Tensor, offsets, counts,
     desc, n, H, I = _grouped_fp8(x, offsets, counts, w1, m_cap, max_rows, "w1")
     if gather:
         desc.num_tokens, desc.top_k = rows, top_k
+    desc.fast = bool(fast)
     _need_fp8(x, x_scale, "x", (rows, H), (rows, _runs(H)))
     for w, s, name in ((w1, w1_scale, "w1"), (w3, w3_scale, "w3")):
         _need_fp8(w, s, name, (n, I, H), (n, _runs(I), _runs(H)))

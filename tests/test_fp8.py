@@ -241,7 +241,7 @@ def test_linear_fp8_argument_checks_launch_nothing():
 
 def _grouped_desc(**kw):
     from combine_top_router_amd._lib import GroupedFp8Desc
-    d = dict(m_cap=256, max_rows=256, num_tokens=64, num_groups=2, inner=128, cols=128, top_k=2)
+    d = dict(m_cap=256, max_rows=256, num_tokens=64, num_groups=2, inner=128, cols=128, top_k=2, fast=0, reserved=0)
     d.update(kw)
     return GroupedFp8Desc(*(d[k] for k, _ in GroupedFp8Desc._fields_))
 
@@ -262,6 +262,7 @@ def test_grouped_fp8_argument_checks_launch_nothing():
         for bad, status in ((dict(m_cap=-1), 1), (dict(max_rows=-1), 1), (dict(num_groups=0), 1),
                             (dict(num_groups=1025), 1), (dict(inner=0), 1), (dict(cols=0), 1),
                             (dict(inner=(1 << 20) + 128), 1), (dict(cols=(1 << 20) + 128), 1),
+                            (dict(fast=2), 1), (dict(reserved=1), 1),
                             (dict(inner=192), 2), (dict(cols=192), 2), (dict(m_cap=1 << 31), 2),
                             (dict(m_cap=(1 << 31) - 1, cols=1 << 20), 2)):
             assert call(fn, names, _grouped_desc(**bad)) == status, (fn, bad)
