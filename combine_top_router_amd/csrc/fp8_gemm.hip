@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kThreads8) void fp8_rows_kernel(Fp8Args g) {
       if (kt + kWaves8 * d < KT) {
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
-          const f32x4 p = run_product<true>(join(x.w[0], x.w[1]), join(x.a[i][0], x.a[i][1]));
+          const f32x4 p = run_product_exact(join(x.w[0], x.w[1]), join(x.a[i][0], x.a[i][1]));
           const float s = x.s[i] * x.sw;
 #pragma unroll
           for (int q = 0; q < 4; ++q) sum[i][q] = __builtin_fmaf(p[q], s, sum[i][q]);
@@ -105,6 +105,9 @@ __global__ __launch_bounds__(kThreads8) void fp8_rows_kernel(Fp8Args g) {
 // ---- host
 
 constexpr int kFewRows = 64;
+#ifndef GBM
+#define GBM 160
+#endif
 
 struct Tile8 {
   int bm, bn;
@@ -231,7 +234,7 @@ hipError_t launch_gate_up_fp8(const moe_grouped_fp8_desc& d, const void* x, cons
   g.gather = src_row, g.top_k = d.top_k, g.tokens = d.num_tokens;
   g.h = static_cast<uint8_t*>(h), g.hs = hs;
   if (d.fast) return launch8<kGated, 256, 256, 2>(g, INT64_MAX, s);
-  return launch8<kGated, 192, 256, 2, true>(g, INT64_MAX, s);
+  return launch8<kGated, GBM, 256, 2, true>(g, INT64_MAX, s);
 }
 
 hipError_t launch_down_fp8(const moe_grouped_fp8_desc& d, const void* h, const float* hs,
