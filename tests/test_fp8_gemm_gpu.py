@@ -105,6 +105,14 @@ def test_linear_long_and_split(M, K, N):
     check_linear(ops.linear_fp8(x, xs, w, ws), xv, wv)
 
 
+@pytest.mark.parametrize("M", [1, 16, 20, 40, 64, 70])
+@pytest.mark.parametrize("K, N", [(272, 6144), (1280, 6201), (128, 9000)])
+def test_linear_few_rows_many_columns(M, K, N):
+    x, xs, xv = row_operand(M, K, 25)
+    w, ws, wv = weight_operand(N, K, 27)
+    check_linear(ops.linear_fp8(x, xs, w, ws), xv, wv)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("M, K, N", [(5, 256, 72), (40, 1040, 37), (150, 384, 264), (300, 272, 515), (90, 8192, 130)])
