@@ -376,6 +376,14 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     sb[0] = *reinterpret_cast<const float*>(smem + x.w);
     sb[1] = GATED ? *reinterpret_cast<const float*>(smem + x.w + 256) : sb[0];
   };
+  // Waits for a range's first slice. Of the tile before, `stores` stores at least were issued
+  // behind the slices' loads; loads and stores complete in order, so those may be outstanding too.
+  int stores = 0;
+  auto wait_first = [&]() __attribute__((always_inline)) {
+    if (stores >= 16) wait_vmcnt<(NS - 1) * NL + 16>();
+    else if (stores >= 8) wait_vmcnt<(NS - 1) * NL + 8>();
+    else wait_vmcnt<(NS - 1) * NL>();
+  };
   auto scaled_add = [&](f32x4& to, const f32x4& p, float s) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) to[q] = __builtin_fmaf(p[q], s, to[q]);
@@ -388,7 +396,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     f32x4 part[4];
     float sa[4], sb[2], s_old[2];
     Place x = place();
-    wait_vmcnt<(NS - 1) * NL>();
+    wait_first();
     __syncthreads();
     read_sw(x, sb);
     read_sa(x, 0, sa);
@@ -491,7 +499,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     auto convert = [&](f16v8& to, const i32x8& from, int q) __attribute__((always_inline)) {
       to = to_f16(from[2 * q], from[2 * q + 1]);
     };
-    wait_vmcnt<(NS - 1) * NL>();
+    wait_first();
     __syncthreads();
     read_sw(x, sb);
     read_sa(x, 0, sa);
@@ -626,22 +634,49 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     } else if constexpr (WIDE) {
       const bool parts = KIND == kDense && g.splits > 1;
       const int64_t nw = t.n0 + wn * 64;
+      if (KIND == kGrouped || (!parts && !g.e.bias && !g.e.res && g.e.act == MOE_ACT_NONE && !g.e.out_f32)) {
+        // nothing to do but to round and to store
+        const int64_t first = (t.row0 + wm * 16 + r15) * g.e.ldo + nw + 8 * grp;
+        uint16_t* o = static_cast<uint16_t*>(g.e.out) + first;
+#pragma unroll
+        for (int i = 0; i < MB; ++i, o += WM * 16 * g.e.ldo) {
+          if ((i * WM + wm) * 16 + r15 >= t.rows) continue;
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            if (nw + 32 * jj + 8 * grp >= N) continue;
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = acc[i][2 * jj + (q >> 2)][q & 3];
+            __builtin_nontemporal_store(KIND == kGrouped ? pack8(v) : pack8x16(v, g.e.f16),
+                                        reinterpret_cast<u32x4*>(o + 32 * jj));
+          }
+        }
+        return;
+      }
       float bias[2][8];
       if (!parts) {
         column_bias(nw + grp * 8, bias[0]);
         column_bias(nw + 32 + grp * 8, bias[1]);
       }
       const Block b(g.e, t.row0, nw);
+      // the residual, a block ahead of its use
+      const bool has_res = KIND == kDense && !parts && g.e.res;
+      u32x4 res[2];
+      auto fetch = [&](int i) __attribute__((always_inline)) {
+        const int r = (i * WM + wm) * 16 + r15;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int c = 32 * jj + 8 * grp;
+          if (r < t.rows && nw + c < N) res[jj] = load8x16(b.res + (r * b.ldr + c));
+        }
+      };
+      if (has_res) fetch(0);
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
         const int r = (i * WM + wm) * 16 + r15;
         if ((i * WM + wm) * 16 >= t.rows) continue;
-        u32x4 res[2];
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          const int c = 32 * jj + 8 * grp;
-          if (!parts && g.e.res && r < t.rows && nw + c < N) res[jj] = load8x16(b.res + (int64_t(r) * g.e.ldr + c));
-        }
+        const u32x4 now[2] = {res[0], res[1]};
+        if (has_res && i + 1 < MB) fetch(i + 1);
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
           const int c = 32 * jj + 8 * grp;
@@ -654,7 +689,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
             *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
             *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
           } else {
-            finish8(g.e, b, r, c, v, bias[jj], res[jj]);
+            finish8(g.e, b, r, c, v, bias[jj], now[jj]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);  // one block's values at a time in registers
@@ -722,6 +757,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     with_blocks<MB, RAGGED ? 1 : 2>(nb, [&](auto b) __attribute__((always_inline)) { reduce(b, k0, k1); });
     if constexpr (!RAGGED) {
       if (k1 < end) {
+        stores = 0;
         first_slices(k1, end);
         reduce(std::integral_constant<int, MB>{}, k1, end);
       }
@@ -736,6 +772,9 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
     if constexpr (WIDE) {
       begin(t);  // the next tile's first slices are on their way during this one's epilogue
       epilogue(now);
+      // each row block with rows in it stores once, or twice where the columns are all there
+      const int blocks = now.rows > wm * 16 ? (now.rows - wm * 16 + 16 * WM - 1) / (16 * WM) : 0;
+      stores = GATED ? blocks : now.n0 + wn * 64 + 64 <= N ? 2 * blocks : 0;
     } else {
       epilogue(now);
       __syncthreads();  // LDS is read out before it is written again
