@@ -27,6 +27,9 @@ def _ptr(t):
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous() and
+            (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device.type != "cuda":
@@ -374,6 +377,9 @@ _LINEAR_ROWS = {torch.bfloat16: 0, torch.float16: 1}
 
 def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> int:
     """Checks a [rows, cols] tensor whose rows may lie apart; returns their stride."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and
+            shape[0] > 1 and t.stride(1) == 1 and t.stride(0) >= shape[1]):
+        return t.stride(0)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device.type != "cuda":
