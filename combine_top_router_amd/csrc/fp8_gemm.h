@@ -16,6 +16,7 @@ constexpr int kMaxGroups = 1024;
 constexpr int kWaves8 = 8;
 constexpr int kThreads8 = 64 * kWaves8;
 constexpr uint32_t kPast = 0x80000000u;  // a byte offset past every buffer range
+constexpr int kGroupsPer = kMaxGroups / kThreads8;  // groups a thread counts
 constexpr int kBandRows = 4;             // row tiles walked together
 
 // kDense    one group of M rows, c through the linear layer's epilogue
@@ -117,24 +118,31 @@ __device__ __forceinline__ void with_blocks(int nb, F&& f) {
   f(std::integral_constant<int, MB>{});
 }
 
+// The ragged kinds' groups: row tiles before each, rows, first row; sums of the wavefronts.
+struct Groups {
+  int prefix[kMaxGroups + 1], cnt[kMaxGroups], off[kMaxGroups], wave[2 * kWaves8];
+};
+struct NoGroups {};
+
+template <int BM, int BN>
+constexpr int stage_bytes() {  // rows of a (wave-loads of 64), rows of w, the scales
+  return (BM + 63) / 64 * 64 * kRun + BN * kRun + kThreads8 * 4;
+}
+
+// The tiles of BM rows x BN staged rows of w, through NS stages.
 // WIDE: rows of the outputs go out in 16-byte pieces (always so for the ragged kinds).
 // EXACT: products in fp16
-template <int BM, int BN, int NS, int KIND, bool WIDE, bool EXACT>
-__global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
+template <int BM, int BN, int NS, int KIND, bool WIDE, bool EXACT, class GroupsT>
+__device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, GroupsT& groups, uint32_t* amax_s) {
   constexpr bool GATED = KIND == kGated, RAGGED = KIND != kDense;
   constexpr int WN = BN / 64, WM = kWaves8 / WN, MB = BM / WM / 16;  // a wavefront: 16 MB rows x 64 staged columns
   constexpr int OUT = GATED ? BN / 2 : BN;  // output columns of a tile
-  constexpr int A_BYTES = (BM + 63) / 64 * 64 * kRun, B_BYTES = BN * kRun, S_BYTES = kThreads8 * 4;
-  constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
+  constexpr int A_BYTES = (BM + 63) / 64 * 64 * kRun, B_BYTES = BN * kRun;
+  constexpr int STAGE = stage_bytes<BM, BN>();
   constexpr int AL = (BM + 63) / 64, BL = BN / 64, NL = AL + BL + 1;  // wave-loads of a slice
   constexpr int MS = (MB + 1) / 2 * 2;   // places of a row's scales in a stage
   constexpr int SW = (WM * 16 * MS + 63) / 64;  // the wavefront that brings w's scales; those before it bring the rows'
   static_assert(MB >= 2 && WM * WN == kWaves8 && SW + 1 < kWaves8, "tile");
-  __shared__ __attribute__((aligned(1024))) char smem[NS * STAGE];
-  // of each group: the row tiles before it, its rows, its first row
-  __shared__ int mt_prefix[RAGGED ? kMaxGroups + 1 : 1], cnt_s[RAGGED ? kMaxGroups : 1],
-      off_s[RAGGED ? kMaxGroups : 1], wave_tot[kWaves8];
-  __shared__ uint32_t amax_s[GATED ? WN * BM : 1];
 
   const int tid = threadIdx.x, lane = lane_id(), wid = uniform(tid / kWave);
   const int wm = wid / WN, wn = wid % WN;
@@ -144,41 +152,36 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
 
   int total;
   if constexpr (RAGGED) {
-    // a group's rows stay inside [0, m_cap) whatever the device's counts say
-    constexpr int PER = kMaxGroups / kThreads8;
-    int v[PER], run = 0;
+    // (so many groups over the same rows that their tiles pass kManyTiles compute nothing: sums stop there)
+    constexpr int kManyTiles = (1 << 30) - 1;
+    int v[kGroupsPer], run = 0;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int e = tid * PER + q;
-      int c = 0;
-      if (e < g.groups) {
-        const int o = g.offsets[e];
-        const int64_t room = o < 0 ? 0 : max(int64_t(0), g.m_cap - o);
-        c = int(min(int64_t(min(max(g.counts[e], 0), g.max_rows)), room));
-        cnt_s[e] = c, off_s[e] = o;
-      }
-      v[q] = (c + BM - 1) / BM;
+    for (int q = 0; q < kGroupsPer; ++q) {
+      const int e = tid * kGroupsPer + q;
+      v[q] = e < g.groups ? (groups.cnt[e] + BM - 1) / BM : 0;
       run += v[q];
     }
     int incl = run;
 #pragma unroll
     for (int off = 1; off < kWave; off <<= 1) {
       const int o = __shfl_up(incl, off, kWave);
-      if (lane >= off) incl += o;
+      if (lane >= off) incl = min(incl + o, kManyTiles);
     }
-    if (lane == kWave - 1) wave_tot[wid] = incl;
+    if (lane == kWave - 1) groups.wave[wid] = incl;
     __syncthreads();
-    int ex = incl - run;
-    for (int w = 0; w < wid; ++w) ex += wave_tot[w];
+    const int before = __shfl_up(incl, 1, kWave);
+    int ex = lane > 0 ? before : 0;
+    for (int w = 0; w < wid; ++w) ex = min(ex + groups.wave[w], kManyTiles);
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int e = tid * PER + q;
-      if (e < g.groups) mt_prefix[e] = ex;
-      ex += v[q];
+    for (int q = 0; q < kGroupsPer; ++q) {
+      const int e = tid * kGroupsPer + q;
+      if (e < g.groups) groups.prefix[e] = ex;
+      ex = min(ex + v[q], kManyTiles);
     }
-    if (tid == kThreads8 - 1) mt_prefix[g.groups] = ex;
+    if (tid == kThreads8 - 1) groups.prefix[g.groups] = ex;
     __syncthreads();
-    total = uniform(mt_prefix[g.groups]) * NT;
+    const int64_t all = int64_t(uniform(groups.prefix[g.groups])) * NT;
+    total = all < kManyTiles ? int(all) : 0;
   } else {
     total = g.tiles_m * NT * g.splits;
   }
@@ -201,13 +204,13 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
       int lo = 0, hi = g.groups - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (mt_prefix[mid] * NT <= id) lo = mid; else hi = mid - 1;
+        if (groups.prefix[mid] * NT <= id) lo = mid; else hi = mid - 1;
       }
       t.e = uniform(lo);
       t.split = 0;
-      mtiles = uniform(mt_prefix[t.e + 1] - mt_prefix[t.e]);
-      rem = id - uniform(mt_prefix[t.e]) * NT;
-      rows = uniform(cnt_s[t.e]);
+      mtiles = uniform(groups.prefix[t.e + 1] - groups.prefix[t.e]);
+      rem = id - uniform(groups.prefix[t.e]) * NT;
+      rows = uniform(groups.cnt[t.e]);
     } else {
       const int tiles = g.tiles_m * NT;
       t.e = 0;
@@ -233,7 +236,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
       const int blks = (rows + 15) / 16, bq = blks / mtiles, br = blks % mtiles;
       const int start = 16 * (mt * bq + min(mt, br));
       t.rows = min((bq + (mt < br ? 1 : 0)) * 16, rows - start);
-      t.row0 = int64_t(uniform(off_s[t.e])) + start;
+      t.row0 = int64_t(uniform(groups.off[t.e])) + start;
     } else {
       t.row0 = int64_t(mt) * BM;
       t.rows = uniform(int(min(int64_t(BM), g.M - t.row0)));
@@ -803,6 +806,54 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
       begin(t);
     }
   }
+}
+
+// FEW > 0: row tiles of FEW rows with a third stage, where the groups are so small that this makes
+// few more tiles: less of a stage is rows that are not there, and more of w is on its way. 32 groups,
+// 7168 and 2048 wide, gate/up with 160 rows a tile and down with 256 against 64: groups of 32
+// rows 205 -> 168 us and 127 -> 104, of 128 251 -> 316 and 138 -> 136, of 256 486 -> 574 and
+// 182 -> 244; skewed groups with 1.22 times the tiles 223 -> 208 and 119 -> 101, with 1.47 times
+// 204 -> 227 and 121 -> 116. So gate/up (twice the operands of a tile to read again) takes them up to 5/4
+// times the tiles, down up to twice.
+template <int BM, int BN, int NS, int KIND, bool WIDE, bool EXACT, int FEW>
+__global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
+  constexpr bool RAGGED = KIND != kDense;
+  constexpr int LDS = NS * stage_bytes<BM, BN>(), LDS_FEW = FEW ? 3 * stage_bytes<FEW ? FEW : BM, BN>() : 0;
+  __shared__ __attribute__((aligned(1024))) char smem[LDS > LDS_FEW ? LDS : LDS_FEW];
+  __shared__ std::conditional_t<RAGGED, Groups, NoGroups> groups;
+  __shared__ uint32_t amax_s[KIND == kGated ? BN / 64 * BM : 1];
+  if constexpr (RAGGED) {
+    // a group's rows stay inside [0, m_cap) whatever the device's counts say
+    const int tid = threadIdx.x;
+    int tiles = 0, few = 0;
+#pragma unroll
+    for (int q = 0; q < kGroupsPer; ++q) {
+      const int e = tid * kGroupsPer + q;
+      if (e >= g.groups) continue;
+      const int o = g.offsets[e];
+      const int64_t room = o < 0 ? 0 : max(int64_t(0), g.m_cap - o);
+      const int c = int(min(int64_t(min(max(g.counts[e], 0), g.max_rows)), room));
+      groups.cnt[e] = c, groups.off[e] = o;
+      tiles += (c + BM - 1) / BM;
+      if constexpr (FEW > 0) few += min((c + FEW - 1) / FEW, 1 << 16);
+    }
+    if constexpr (FEW > 0) {
+      tiles = min(tiles, 1 << 16);
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1)
+        tiles += __shfl_xor(tiles, off, kWave), few += __shfl_xor(few, off, kWave);
+      const int wid = tid / kWave;
+      if (lane_id() == 0) groups.wave[wid] = tiles, groups.wave[kWaves8 + wid] = few;
+      __syncthreads();
+      tiles = few = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves8; ++w) tiles += groups.wave[w], few += groups.wave[kWaves8 + w];
+      __syncthreads();
+      if (uniform(few) * 4 <= uniform(tiles) * (KIND == kGated ? 5 : 8))
+        return fp8_tiles<FEW, BN, 3, KIND, WIDE, EXACT>(g, smem, groups, amax_s);
+    }
+  }
+  fp8_tiles<BM, BN, NS, KIND, WIDE, EXACT>(g, smem, groups, amax_s);
 }
 
 // The sums of the splits, in order, and the epilogue: eight columns a thread.

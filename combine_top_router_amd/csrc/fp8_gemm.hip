@@ -1,4 +1,35 @@
 // Products of 8-bit operands on the matrix cores: dense, and grouped by expert.
+//
+//   z[m, n] = sum over runs b of sa[m, b] sw[n / 128, b] p_b[m, n],
+//   p_b[m, n] = sum over k in [128 b, 128 b + 128) of a[m, k] w[n, k]
+//
+// A run is as long as one 16x16x128 instruction: its sum starts from zero, is scaled by an fp32
+// factor of its row and its block of columns and added in fp32, so that each product costs one matrix
+// instruction and four vector additions for 16 x 16 outputs. Both operands lie with k last,
+// w output-major; the product is taken as w a^T, which leaves four neighbouring columns of a row
+// in a lane and 16-byte stores.
+//
+//   fp8_kernel       tiles of 64 .. 256 rows x 128 or 256 columns, one workgroup of eight
+//                    wavefronts to a CU, that walks its tiles: two to four stages of a 128-long
+//                    slice of both operands in LDS, filled by loads that go there directly, the
+//                    chunks swizzled so that 16 rows' fragments lie in 16 bank groups; products in
+//                    an order that frees fragments early (block_of); a tile's first slices are
+//                    loaded during the epilogue of the tile before it.
+//   fp8_rows_kernel  up to 64 rows: 16 or 32 columns to a workgroup, the reduction shared out among
+//                    its wavefronts, each with a ring of its own.
+//   fp8_join_kernel  the sums of a reduction split over workgroups, in order, and the epilogue.
+//
+// Two ways to a run's sum (run_product, run_product_exact): the 8-bit instruction, which loses
+// 1.4e-5, for outputs of 16 bits; and fp16 copies of the values at half its rate.
+//
+// Bound, with many rows: the matrix cores and their clock (1.7 to 1.9 GHz under this load). 8192x8192x8192
+// takes 450 us, 2440 TFLOP/s; a product with one scale for all, which needs no vector work,
+// reaches 2816 on the same card. Beside a product about five vector instructions are free, the
+// scaled addition and its scale take five: a sixth cost a fifth of the time. 65536x2048x7168
+// (few slices to a tile): 949 us, 2030 TFLOP/s, and with a residual 1135: its loads come
+// between the stores of 256 KB a tile.
+// Few rows: one read of w. 16x7168x4096: 10.2 us, 2.9 TB/s; 32 experts' gate/up, 7168 -> 2048,
+// 32 rows each: 168 us, 5.6 TB/s; down 104 us, 4.5 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <iterator>
@@ -8,7 +39,8 @@
 namespace moe {
 namespace {
 
-// Few rows (16 RB at most): bound by reading w once. A workgroup takes 16 CB columns, its
+// Few rows (16 RB at most): bound by reading w once, and of a single call by the time that a
+// chip full of first loads takes (16x7168x4096: 10.2 us, 29 MB). A workgroup takes 16 CB columns, its
 // WAVES wavefronts an equal share of the runs each, through a ring of D runs in LDS that is
 // the wavefront's own: no barrier until the wavefronts' sums meet in LDS at the end. (Fragments
 // read from memory as they are needed, 16 rows x 64 bytes each, took half as long again:
@@ -136,9 +168,12 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(Fp8Args g) {
 // ---- host
 
 constexpr int kFewRows = 64;
-#ifndef GBM
-#define GBM 160
-#endif
+// Row tile of gate/up at full width. Its fp16 fragments leave no registers for more than 192 rows.
+// 32 groups of 7168 -> 2048, with 128, 160, 192 rows a tile: groups of 160 rows 363, 282, 300 us; of
+// 192 366, 379, 332; of 256 451, 455, 467; of 320 611, 544, 550; around 256 +- 16 520, 479, 484;
+// of 512 859, 872, 856; of 2048 3238, 3130, 3122.
+constexpr int kGatedRows = 160;
+constexpr int kFewTile = 64;  // row tile of the grouped products where groups are small
 
 // A tile shape with what its workgroups take, in microseconds: a slice with the whole chip at
 // work, as a share of that on a quiet chip, and a workgroup's beginning and end without its
@@ -212,10 +247,13 @@ Plan8 plan8(int64_t M, int64_t N, int64_t K, bool exact) {
 template <int KIND, int BM, int BN, int NS, bool EXACT = false>
 hipError_t launch8(const Fp8Args& g, int64_t tiles, hipStream_t s) {
   const int grid = static_cast<int>(std::min<int64_t>(tiles, device_cu_count()));
-  if (KIND == kDense && !g.e.vec && g.splits == 1)
-    fp8_kernel<BM, BN, NS, KIND, KIND != kDense, EXACT><<<grid, kThreads8, 0, s>>>(g);
-  else
-    fp8_kernel<BM, BN, NS, KIND, true, EXACT><<<grid, kThreads8, 0, s>>>(g);
+  if constexpr (KIND != kDense) {
+    fp8_kernel<BM, BN, NS, KIND, true, EXACT, kFewTile><<<grid, kThreads8, 0, s>>>(g);
+  } else if (!g.e.vec && g.splits == 1) {
+    fp8_kernel<BM, BN, NS, KIND, false, EXACT, 0><<<grid, kThreads8, 0, s>>>(g);
+  } else {
+    fp8_kernel<BM, BN, NS, KIND, true, EXACT, 0><<<grid, kThreads8, 0, s>>>(g);
+  }
   return hipGetLastError();
 }
 
@@ -308,7 +346,7 @@ hipError_t launch_gate_up_fp8(const moe_grouped_fp8_desc& d, const void* x, cons
   g.gather = src_row, g.top_k = d.top_k, g.tokens = d.num_tokens;
   g.h = static_cast<uint8_t*>(h), g.hs = hs;
   if (d.fast) return launch8<kGated, 256, 256, 2>(g, INT64_MAX, s);
-  return launch8<kGated, GBM, 256, 2, true>(g, INT64_MAX, s);
+  return launch8<kGated, kGatedRows, 256, 2, true>(g, INT64_MAX, s);
 }
 
 hipError_t launch_down_fp8(const moe_grouped_fp8_desc& d, const void* h, const float* hs,

@@ -403,3 +403,84 @@ def test_error_on_normal_values(M, K, N):
     for dt, most in ((torch.float32, 2e-6), (torch.bfloat16, HALF[torch.bfloat16]), (torch.float16, HALF[torch.float16])):
         y = np64(ops.linear_fp8(x, xs, w, ws, out_dtype=dt))
         assert np.linalg.norm(y - want) <= most * np.linalg.norm(want), dt
+
+
+def far_rows(M, K, few, seed):
+    """(q, scale, the last rows' values): zeros but for the last `few` rows."""
+    q = torch.zeros((M, K), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    s = torch.zeros((M, -(-K // 128)), device=DEV)
+    fq, fs, v = row_operand(few, K, seed)
+    q.view(torch.uint8)[-few:] = fq.view(torch.uint8)
+    s[-few:] = fs
+    return q, s, v
+
+
+@pytest.mark.parametrize("K, N", [(2048, 128), (128, 2048)])
+def test_rows_past_32_bits(K, N):
+    M, few = 2200000, 300  # 4.5e9 elements of x or of y
+    x, xs, xv = far_rows(M, K, few, 70)
+    w, ws, wv = weight_operand(N, K, 72)
+    y = ops.linear_fp8(x, xs, w, ws)
+    check_linear(y[-few:], xv, wv, exact=False)
+    del y
+    off = torch.tensor([0, M - few, M], dtype=torch.int32, device=DEV)
+    cnt = torch.tensor([10, few], dtype=torch.int32, device=DEV)
+    y = ops.grouped_down_fp8(x, xs, off, cnt, torch.stack([w.view(torch.uint8)] * 2).view(w.dtype), torch.stack([ws] * 2))
+    check_linear(y[-few:], xv, wv, exact=False)
+    del y
+    w3, s3, v3 = weight_operand(N, K, 74, 2)
+    h, hs = ops.grouped_gate_up_fp8(x, xs, off, cnt, torch.stack([w.view(torch.uint8)] * 2).view(w.dtype),
+                                    torch.stack([ws] * 2), w3, s3)
+    check_h(h[-few:], hs[-few:], slice(None), xv, wv, v3[1], "far rows")
+
+
+@pytest.mark.parametrize("M", [16, 100])
+def test_weights_past_32_bits(M):
+    N, K, few = 1 << 20, 4352, 256  # 4.6e9 elements
+    x, xs, xv = row_operand(M, K, 76)
+    w = torch.zeros((N, K), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    ws = torch.zeros((N // 128, K // 128), device=DEV)
+    lw, ls, wv = weight_operand(few, K, 80)
+    w.view(torch.uint8)[-few:] = lw.view(torch.uint8)
+    ws[-few // 128:] = ls
+    y = ops.linear_fp8(x, xs, w, ws)
+    assert (y[:, :-few] == 0).all()
+    check_linear(y[:, -few:], xv, wv, exact=M <= 64)
+
+
+def test_experts_past_32_bits():
+    E, N, K, few = 520, 2048, 4096, 40  # 4.4e9 elements of each matrix stack
+    x, xs, xv = row_operand(few, K, 82)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    cnt = torch.zeros(E, dtype=torch.int32, device=DEV)
+    off[E], cnt[E - 1] = few, few
+    w = [torch.zeros((E, N, K), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+    s = [torch.zeros((E, N // 128, K // 128), device=DEV) for _ in range(2)]
+    v = []
+    for i in range(2):
+        q, sc, val = weight_operand(N, K, 84 + 2 * i)
+        w[i].view(torch.uint8)[-1], s[i][-1] = q.view(torch.uint8), sc
+        v.append(val)
+    h, hs = ops.grouped_gate_up_fp8(x, xs, off, cnt, w[0], s[0], w[1], s[1])
+    check_h(h, hs, slice(None), xv, v[0], v[1], "last expert")
+    y = ops.grouped_down_fp8(x, xs, off, cnt, w[0], s[0])
+    check_linear(y, xv, v[0], exact=False)
+
+
+def test_two_calls_at_once():
+    """Split products on two streams, each with its own workspace, give what they give alone."""
+    M, K, N = 70, 4096, 256
+    w, ws, _ = weight_operand(N, K, 90)
+    rows = [row_operand(M, K, 92 + 2 * i)[:2] for i in range(2)]
+    assert ops.linear_fp8_workspace_bytes(rows[0][0], w) > 0
+    alone = [ops.linear_fp8(*r, w, ws) for r in rows]
+    streams = [torch.cuda.Stream() for _ in rows]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(ops.linear_fp8(*rows[i], w, ws))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, alone[i]) for y in got[i])

@@ -272,3 +272,41 @@ def test_refusals():
         ops.quantize_fp8_weights(x[:, :40].contiguous())
     with pytest.raises(ValueError, match="must be contiguous"):
         ops.quantize_fp8_weights(x.t())
+
+
+def test_rows_past_32_bits():
+    rows, hidden, few = 300000, 16384, 5  # 4.9e9 elements
+    x = torch.zeros((rows, hidden), dtype=torch.bfloat16, device=DEV)
+    x[-few:] = rnd((few, hidden), torch.bfloat16, 40)
+    gain = rnd((hidden,), torch.float32, 41)
+    y, q, s, _ = ops.rms_norm(x, gain, want_fp8=True)
+    wy, wq, ws, _ = ops.rms_norm(x[-few:], gain, want_fp8=True)
+    # (rows this wide take the same kernel whatever their number)
+    assert torch.equal(y[-few:], wy) and torch.equal(q[-few:].view(torch.uint8), wq.view(torch.uint8))
+    assert torch.equal(s[-few:], ws)
+    del y, q, s
+    q, s = ops.quantize_fp8(x)
+    wq, ws = fp8.rows(x[-few:].float().cpu().numpy())
+    assert (bytes_of(q[-few:]) == wq).all() and (s[-few:].cpu().numpy() == ws).all()
+    del q, s
+    dy = torch.zeros_like(x)
+    dy[-few:] = rnd((few, hidden), torch.bfloat16, 42)
+    dx, dg = ops.rms_norm_backward(dy, x, gain)
+    wdx, wdg = ops.rms_norm_backward(dy[-few:], x[-few:], gain)
+    assert torch.equal(dx[-few:], wdx)
+    # the same terms dy xhat, added in the same order or another by at most `few` roundings each way
+    h = np64(x[-few:])
+    terms = np.abs(np64(dy[-few:]) * h * norm.rstd(h, 1e-6)).sum(axis=0)
+    close(dg, np64(wdg), 2 * few * 2.0 ** -24 * terms)
+
+
+def test_weights_past_32_bits():
+    n, N, K = 1100, 2048, 2048  # 4.6e9 elements
+    w = torch.zeros((n, N, K), dtype=torch.bfloat16, device=DEV)
+    w[-1] = rnd((N, K), torch.bfloat16, 43)
+    for turn in (False, True):
+        q, s = ops.quantize_fp8_weights(w, transpose=turn)
+        v = w[-1].t() if turn else w[-1]
+        wq, ws = fp8.weights(v.float().cpu().numpy())
+        assert (bytes_of(q[-1]) == wq).all() and (s[-1].cpu().numpy() == ws).all()
+        del q, s
