@@ -16,7 +16,7 @@
 // (fp64), so that the result does not depend on timing.
 // Bound: HBM. A workgroup walks several rows and keeps the gain in registers.
 // 65536 x 7168 bf16 with residual, total and 8-bit output: 615 us, 5.4 TB/s (a large copy
-// reaches 4.9); the gradients of 16384 x 7168: 196 us, 4.8 TB/s.
+// reaches 4.9); the gradients of 16384 x 7168: 187 us, 5.0 TB/s.
 #include <algorithm>
 
 #include "../../include/moe.h"
@@ -242,32 +242,41 @@ __global__ __launch_bounds__(64 * block_waves<WAVES>()) void norm_grad_kernel(No
   }
 }
 
-// dgain[c] = the workgroups' sums, in order: 16 columns to a workgroup, each of its
-// 16 row lanes every 16th of them.
-__global__ __launch_bounds__(256) void gain_grad_kernel(const float* sums, int blocks, int H,
-                                                        float* dgain) {
-  __shared__ double part[16][17];
-  const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
-  const int n = int(blockIdx.x) * 16 + c;
-  double s = 0.0;
+// dgain[c] = the workgroups' sums, in a fixed order: 32 columns to a workgroup, whole lines of a
+// sum's row to eight lanes, every 128th row to a lane. (768 sums of 7168: 8 us; 18 with half lines
+// and 16 lanes to a column, whose batches of loads waited for each other.)
+__global__ __launch_bounds__(1024) void gain_grad_kernel(const float* sums, int blocks, int H,
+                                                         float* dgain) {
+  __shared__ double part[16][32];
+  const int c = (threadIdx.x & 7) * 4, q = threadIdx.x >> 3;
+  const int n = int(blockIdx.x) * 32 + c;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
   if (n < H) {
     constexpr int kBatch = 8;  // loads in flight together
-    for (int b = q; b < blocks; b += 16 * kBatch) {
-      float x[kBatch];
+    for (int b = q; b < blocks; b += 128 * kBatch) {
+      f32x4 x[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
-        x[u] = b + 16 * u < blocks ? sums[int64_t(b + 16 * u) * H + n] : 0.f;
+        x[u] = b + 128 * u < blocks ? *reinterpret_cast<const f32x4*>(sums + int64_t(b + 128 * u) * H + n)
+                                    : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) s += double(x[u]);
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += double(x[u][i]);
     }
   }
-  part[q][c] = s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int off = 8; off < kWave; off <<= 1) s[i] += __shfl_xor(s[i], off, kWave);
+    if (lane_id() < 8) part[threadIdx.x / kWave][c + i] = s[i];
+  }
   __syncthreads();
-  if (q == 0 && n < H) {
+  if (threadIdx.x < 32 && int(blockIdx.x) * 32 + int(threadIdx.x) < H) {
     double t = 0.0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += part[i][c];
-    dgain[n] = static_cast<float>(t);
+    for (int w = 0; w < 16; ++w) t += part[w][threadIdx.x];
+    dgain[blockIdx.x * 32 + threadIdx.x] = static_cast<float>(t);
   }
 }
 
@@ -342,7 +351,7 @@ hipError_t launch_rms_norm_backward(const moe_norm_desc& d, const void* dy, cons
     if (e != hipSuccess) return e;
   }
   if (!dgain) return hipSuccess;
-  gain_grad_kernel<<<(d.hidden + 15) / 16, 256, 0, s>>>(a.sums, grid, d.hidden, dgain);
+  gain_grad_kernel<<<(d.hidden + 31) / 32, 1024, 0, s>>>(a.sums, grid, d.hidden, dgain);
   return hipGetLastError();
 }
 
