@@ -638,28 +638,42 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
       const bool parts = KIND == kDense && g.splits > 1;
       const int64_t nw = t.n0 + wn * 64;
       // Nothing to do but to add a residual, to round and to store: without the general form's
-      // vector work, which took a third of a tile's time at six runs (65536x768x2048: 157 -> 133 us).
+      // vector work, which took a third of a tile's time at six runs (65536x768x2048: 157 -> 133 us, now 129).
+      // Two neighbouring lanes' rows change halves, so that a store, and a load of the residual, takes
+      // 128 bytes of a row and not 64: first the even rows, then the odd ones (65536x2048x7168: 961 -> 919 us,
+      // with a residual 1152 -> 1080).
       auto store_rows = [&](auto res_tag) __attribute__((always_inline)) {
         constexpr bool RES = decltype(res_tag)::value;
-        const int64_t row = t.row0 + wm * 16 + r15, col = nw + 8 * grp;
+        const bool odd = r15 & 1;
+        const int64_t row = t.row0 + wm * 16 + (r15 & ~1), col = nw + 32 * (r15 & 1) + 8 * grp;
+        const bool in = col < N;
         uint16_t* o = static_cast<uint16_t*>(g.e.out) + row * g.e.ldo + col;
         const uint16_t* p = RES ? g.e.res + row * g.e.ldr + col : nullptr;
+        // (x, y): columns 0-31 and 32-63 of the lane's row <-> its part of the even and of the odd row
+        auto trade = [&](u32x4& x, u32x4& y) __attribute__((always_inline)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t a = x[q], b = y[q], got = dpp<0xb1>(odd ? a : b);
+            x[q] = odd ? got : a, y[q] = odd ? b : got;
+          }
+        };
         u32x4 res[2];
         auto fetch = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj)
-            if ((i * WM + wm) * 16 + r15 < t.rows && col + 32 * jj < N) res[jj] = load8x16(p + 32 * jj);
+          const int r = (i * WM + wm) * 16 + (r15 & ~1);
+          if (in && r < t.rows) res[0] = load8x16(p);
+          if (in && r + 1 < t.rows) res[1] = load8x16(p + g.e.ldr);
           p += WM * 16 * g.e.ldr;
         };
         if constexpr (RES) fetch(0);
 #pragma unroll
         for (int i = 0; i < MB; ++i, o += WM * 16 * g.e.ldo) {
-          const u32x4 now[2] = {res[0], res[1]};
+          u32x4 now[2] = {res[0], res[1]};
           if (RES && i + 1 < MB) fetch(i + 1);
-          if ((i * WM + wm) * 16 + r15 >= t.rows) continue;
+          if ((i * WM + wm) * 16 >= t.rows) continue;
+          if constexpr (RES) trade(now[0], now[1]);
+          u32x4 out[2];
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
-            if (col + 32 * jj >= N) continue;
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = acc[i][2 * jj + (q >> 2)][q & 3];
@@ -669,9 +683,12 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
 #pragma unroll
               for (int q = 0; q < 8; ++q) v[q] += x[q];
             }
-            __builtin_nontemporal_store(KIND == kGrouped ? pack8(v) : pack8x16(v, g.e.f16),
-                                        reinterpret_cast<u32x4*>(o + 32 * jj));
+            out[jj] = KIND == kGrouped ? pack8(v) : pack8x16(v, g.e.f16);
           }
+          trade(out[0], out[1]);
+          const int r = (i * WM + wm) * 16 + (r15 & ~1);
+          if (in && r < t.rows) __builtin_nontemporal_store(out[0], reinterpret_cast<u32x4*>(o));
+          if (in && r + 1 < t.rows) __builtin_nontemporal_store(out[1], reinterpret_cast<u32x4*>(o + g.e.ldo));
           if constexpr (RES) __builtin_amdgcn_sched_barrier(0);
         }
       };
@@ -797,9 +814,10 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
     if constexpr (WIDE) {
       begin(t);  // the next tile's first slices are on their way during this one's epilogue
       epilogue(now);
-      // each row block with rows in it stores once, or twice where the columns are all there
+      // each row block with rows in it stores once, or twice where the columns are all there and it
+      // has more than one row
       const int blocks = now.rows > wm * 16 ? (now.rows - wm * 16 + 16 * WM - 1) / (16 * WM) : 0;
-      stores = GATED ? blocks : now.n0 + wn * 64 + 64 <= N ? 2 * blocks : 0;
+      stores = GATED ? blocks : now.n0 + wn * 64 + 64 <= N ? 2 * blocks - (now.rows % 16 == 1) : 0;
     } else {
       epilogue(now);
       __syncthreads();  // LDS is read out before it is written again

@@ -23,11 +23,11 @@
 // 1.4e-5, for outputs of 16 bits; and fp16 copies of the values at half its rate.
 //
 // Bound, with many rows: the matrix cores and their clock (1.7 to 1.9 GHz under this load). 8192x8192x8192
-// takes 450 us, 2440 TFLOP/s; a product with one scale for all, which needs no vector work,
+// takes 435 us, 2530 TFLOP/s; a product with one scale for all, which needs no vector work,
 // reaches 2816 on the same card. Beside a product about five vector instructions are free, the
 // scaled addition and its scale take five: a sixth cost a fifth of the time. 65536x2048x7168
-// (few slices to a tile): 949 us, 2030 TFLOP/s, and with a residual 1135: its loads come
-// between the stores of 256 KB a tile.
+// (few slices to a tile): 919 us, 2090 TFLOP/s, and with a residual 1080: its loads come
+// between the stores of 128 KB a tile.
 // Few rows: one read of w. 16x7168x4096: 10.2 us, 2.9 TB/s; 32 experts' gate/up, 7168 -> 2048,
 // 32 rows each: 168 us, 5.6 TB/s; down 104 us, 4.5 TB/s.
 #include <algorithm>
