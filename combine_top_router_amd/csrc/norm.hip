@@ -16,7 +16,7 @@
 // (fp64), so that the result does not depend on timing.
 // Bound: HBM. A workgroup walks several rows and keeps the gain in registers.
 // 65536 x 7168 bf16 with residual, total and 8-bit output: 615 us, 5.4 TB/s (a large copy
-// reaches 4.9); the gradients of 16384 x 7168: 187 us, 5.0 TB/s.
+// reaches 4.9); the gradients of 16384 x 7168: 186 us, 5.0 TB/s.
 #include <algorithm>
 
 #include "../../include/moe.h"
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * block_waves<WAVES>()) void norm_grad_kernel(No
 }
 
 // dgain[c] = the workgroups' sums, in a fixed order: 32 columns to a workgroup, whole lines of a
-// sum's row to eight lanes, every 128th row to a lane. (768 sums of 7168: 6.6 us; 18 with half lines
+// sum's row to eight lanes, every 128th row to a lane. (768 sums of 7168: 6.3 us; 18 with half lines
 // and 16 lanes to a column, whose batches of loads waited for each other.)
 __global__ __launch_bounds__(1024) void gain_grad_kernel(const float* sums, int blocks, int H,
                                                          float* dgain) {
