@@ -4,6 +4,7 @@
 
 #include "fp8.h"
 #include "linear_epilogue.h"
+#include "slice_range.h"
 
 namespace moe {
 namespace {
@@ -299,41 +300,42 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
       if (lane < left && wid <= SW + (GATED ? 1 : 0)) osc = uint32_t(lane) * uint32_t(KT) * 4u;
     }
   };
-  // Wave-load q of slice kt, by these resources and lane offsets, into the stage at `at`.
+  // Wave-load q of a slice, by these resources and lane offsets, into the stage at `at`.
   struct Sources {
     i32x4 a, b0, b1, s;
+    uint32_t slice;
   };
-  auto load = [&](auto q_tag, const Sources& from, int kt, uint32_t at, const uint32_t (&va)[AL],
+  auto load = [&](auto q_tag, const Sources& from, uint32_t at, const uint32_t (&va)[AL],
                   const uint32_t (&vb)[BL], uint32_t vs) __attribute__((always_inline)) {
     constexpr int q = decltype(q_tag)::value;
     if constexpr (q < BL)
-      load16(GATED && q >= BL / 2 ? from.b1 : from.b0, vb[q], uint32_t(kt) * kRun,
+      load16(GATED && q >= BL / 2 ? from.b1 : from.b0, vb[q], from.slice * kRun,
              at + A_BYTES + (wid + kWaves8 * q) * 1024);
     else if constexpr (q < BL + AL)
-      load16(from.a, va[q - BL], uint32_t(kt) * kRun, at + (wid + kWaves8 * (q - BL)) * 1024);
+      load16(from.a, va[q - BL], from.slice * kRun, at + (wid + kWaves8 * (q - BL)) * 1024);
     else if constexpr (q < NL)
-      load4(from.s, vs, uint32_t(kt) * 4u, at + A_BYTES + B_BYTES + wid * 256);
+      load4(from.s, vs, from.slice * 4u, at + A_BYTES + B_BYTES + wid * 256);
   };
-  // In the loop: a slice at or past `end` reads nothing but zeros, by an empty range. (Scalar
+  // A slice at or past `end` reads nothing but zeros, by an empty range without an offset. (Scalar
   // work: more than about five vector instructions to a product no longer fit beside it.)
   auto upto = [&](int kt, int end) __attribute__((always_inline)) {
-    Sources f{ra, rb0, rb1, rsc};
-    const bool in = kt < end;
-    f.a[2] = in ? ra[2] : 0, f.b0[2] = in ? rb0[2] : 0, f.b1[2] = in ? rb1[2] : 0, f.s[2] = in ? rsc[2] : 0;
+    Sources f{ra, rb0, rb1, rsc, slice_range(kt, end, 0).slice};
+    auto bytes = [&](const i32x4& r) { return int(slice_range(kt, end, uint32_t(r[2])).bytes); };
+    f.a[2] = bytes(ra), f.b0[2] = bytes(rb0), f.b1[2] = bytes(rb1), f.s[2] = bytes(rsc);
     return f;
   };
   // The first slices of a range, all stages; a chunk past K reads zeros too.
   auto first_slices = [&](int k0, int k1) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const int left = k0 + s < k1 ? K - (k0 + s) * kRun : 0;
+      const int left = K - (k0 + s) * kRun;
       uint32_t va[AL], vb[BL];
 #pragma unroll
       for (int i = 0; i < AL; ++i) va[i] = a_ch * 16 < left ? oa[i] : kPast;
 #pragma unroll
       for (int i = 0; i < BL; ++i) vb[i] = b_ch * 16 < left ? ob[i] : kPast;
-      const Sources f{ra, rb0, rb1, rsc};
-      for_each_index([&](auto q) { load(q, f, k0 + s, lds0 + s * STAGE, va, vb, left > 0 ? osc : kPast); },
+      const Sources f = upto(k0 + s, k1);
+      for_each_index([&](auto q) { load(q, f, lds0 + s * STAGE, va, vb, osc); },
                      std::make_integer_sequence<int, NL>{});
     }
   };
@@ -427,7 +429,7 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
       constexpr int PH = decltype(phase_tag)::value, PN = (PH + NB) % 3;
       const uint32_t at = lds0 + stage * STAGE;
       const Sources from = upto(kt + NS, k1);
-      auto load_next = [&](auto q) __attribute__((always_inline)) { load(q, from, kt + NS, at, oa, ob, osc); };
+      auto load_next = [&](auto q) __attribute__((always_inline)) { load(q, from, at, oa, ob, osc); };
       for_each_index([&](auto p_tag) __attribute__((always_inline)) {
         constexpr int p = decltype(p_tag)::value, i = block_of(p, NB), j = column_of(p, NB);
         if constexpr (EARLY && p == 8) __syncthreads();
@@ -523,7 +525,7 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
       constexpr int PH = decltype(phase_tag)::value;
       const uint32_t at = lds0 + stage * STAGE;
       const Sources from = upto(kt + NS, k1);
-      auto load_next = [&](auto q) __attribute__((always_inline)) { load(q, from, kt + NS, at, oa, ob, osc); };
+      auto load_next = [&](auto q) __attribute__((always_inline)) { load(q, from, at, oa, ob, osc); };
       for_each_index([&](auto t_tag) __attribute__((always_inline)) {
         constexpr int t = decltype(t_tag)::value, i = t >> 1, h = t & 1;
         constexpr bool first = t == 0, last = t == 2 * NB - 1;

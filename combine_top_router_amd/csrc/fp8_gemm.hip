@@ -80,18 +80,22 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(Fp8Args g) {
   // run kt into ring slot d; a run past the end, and a chunk past K, zeros
   auto fetch = [&](int d, int kt) __attribute__((always_inline)) {
     const int left = K - kt * kRun;
-    const uint32_t at = ring0 + d * SLOT;
+    const uint32_t at = ring0 + d * SLOT, slice = slice_range(kt, KT, 0).slice;
+    auto upto = [&](i32x4 r) {
+      r[2] = int(slice_range(kt, KT, uint32_t(r[2])).bytes);
+      return r;
+    };
 #pragma unroll
     for (int i = 0; i < 2 * CB; ++i) {
       const int c = (lane & 7) ^ (((i * 8 + lr) >> 1) & 7);
-      load16(rw, c * 16 < left ? ow[i] : kPast, uint32_t(kt) * kRun, at + i * 1024);
+      load16(upto(rw), c * 16 < left ? ow[i] : kPast, slice * kRun, at + i * 1024);
     }
 #pragma unroll
     for (int i = 0; i < 2 * RB; ++i) {
       const int c = (lane & 7) ^ (((i * 8 + lr) >> 1) & 7);
-      load16(ra, c * 16 < left ? oa[i] : kPast, uint32_t(kt) * kRun, at + WB + i * 1024);
+      load16(upto(ra), c * 16 < left ? oa[i] : kPast, slice * kRun, at + WB + i * 1024);
     }
-    load4(rs, left > 0 ? os : kPast, uint32_t(kt) * 4u, at + WB + AB);
+    load4(upto(rs), os, slice * 4u, at + WB + AB);
   };
   f32x4 sum[RB][CB];
 #pragma unroll
