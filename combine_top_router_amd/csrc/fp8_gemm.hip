@@ -19,8 +19,8 @@
 //                    its wavefronts, each with a ring of its own.
 //   fp8_join_kernel  the sums of a reduction split over workgroups, in order, and the epilogue.
 //
-// Two ways to a run's sum (run_product, run_product_exact): the 8-bit instruction, which loses
-// 1.4e-5, for outputs of 16 bits; and fp16 copies of the values at half its rate.
+// Two ways to a run's sum (run_product_exact, run_product): fp16 copies of the values, whose sums keep
+// 24 bits; and where the caller asks for it (fast) the 8-bit instruction, at twice the rate, which loses 1.4e-5.
 //
 // Bound, with many rows: the matrix cores and their clock (1.7 to 1.9 GHz under this load). 8192x8192x8192
 // takes 435 us, 2530 TFLOP/s; a product with one scale for all, which needs no vector work,
@@ -172,11 +172,11 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(Fp8Args g) {
 // ---- host
 
 constexpr int kFewRows = 64;
-// Row tile of gate/up at full width. Its fp16 fragments leave no registers for more than 192 rows.
-// 32 groups of 7168 -> 2048, with 128, 160, 192 rows a tile: groups of 160 rows 363, 282, 300 us; of
+// Row tile of the grouped products at full width. Their fp16 fragments leave no registers for more than
+// 192 rows. Gate/up of 32 groups of 7168 -> 2048, with 128, 160, 192 rows a tile: groups of 160 rows 363, 282, 300 us; of
 // 192 366, 379, 332; of 256 451, 455, 467; of 320 611, 544, 550; around 256 +- 16 520, 479, 484;
 // of 512 859, 872, 856; of 2048 3238, 3130, 3122.
-constexpr int kGatedRows = 160;
+constexpr int kExactRows = 160;
 constexpr int kFewTile = 64;  // row tile of the grouped products where groups are small
 
 // A tile shape with what its workgroups take, in microseconds: a slice with the whole chip at
@@ -186,8 +186,10 @@ struct Tile8 {
   int bm, bn;
   double slice, quiet, fixed, odd;
 };
-constexpr Tile8 kTiles8[] = {{256, 256, 1.62, 0.68, 8.9, 9.0}, {128, 256, 0.81, 0.88, 6.4, 6.1},
-                             {256, 128, 0.91, 0.81, 6.2, 5.4}, {128, 128, 0.55, 0.89, 4.0, 5.1}};
+constexpr Tile8 kFastTiles[] = {{256, 256, 1.61, 0.66, 7.5, 10.4}, {128, 256, 0.83, 0.81, 4.8, 8.0},
+                                {256, 128, 0.91, 0.71, 5.0, 6.7}, {128, 128, 0.54, 0.84, 3.3, 6.0}};
+constexpr Tile8 kExactTiles[] = {{160, 256, 1.79, 0.88, 6.3, 9.0}, {256, 128, 1.59, 0.87, 5.4, 9.3},
+                                 {128, 128, 0.97, 0.97, 3.9, 7.0}, {64, 256, 0.96, 0.98, 3.7, 7.9}};
 constexpr int kSplits8[] = {1, 2, 3, 4, 6, 8, 12, 16};
 
 struct Plan8 {
@@ -196,30 +198,32 @@ struct Plan8 {
 
 // Tile and split of one product, from its sizes alone: the least estimated time. Rounds of
 // workgroups over the chip (slower the more of it works: clock and memory), at least the
-// memory's time, for a split the second launch. The figures are a fit to 58000 timings of these tiles
-// and splits on 4200 products of 65 to 32768 rows, 128 to 12288 terms and 64 to 16384 columns; on
-// them the choice is 1.3 % slower than the best on average. Examples: 8192x8192x8192 takes 256x256
-// (487 us; 128x256 587), 1024x7168x4096 128x128 (40 us; 256x256 87).
-// exact: the fp32 output's products, which the smallest tile alone has.
+// memory's time, for a split the second launch. The figures are fits to timings of these kernels,
+// bf16 out, 65 to 32768 rows, 128 to 12288 terms and 64 to 16384 columns: 113000 of the 8-bit sums' tiles and splits on
+// 8040 products, 88000 of the full-width ones' on 6527. On them the choice is 1.4 and 1.9 % slower than
+// the best on average (a twentieth of them by more than 8 and 9 %). Examples, fast: 8192x4096x4096 takes 256x256
+// (120 us; 128x256 135), 1024x7168x4096 128x128 (37 us; 256x256 76); full width: 8192x8192x8192 160x256
+// (911 us; 192x256, not kept, 944; 128x128 1072), 1024x7168x4096 128x128 (63 us; 160x256 99).
 Plan8 make_plan8(int64_t M, int64_t N, int64_t K, bool exact, double cus) {
   const int64_t runs = (K + kRun - 1) / kRun, nw = (N + 7) / 8 * 8;
   const double mem = (double(M) * K + double(N) * K + double(M) * N * 2.0) / 5.0e6;
   Plan8 best{0, 1, static_cast<int>(runs)};
   double best_t = 1e300;
-  for (int t = exact ? 3 : 0; t < int(std::size(kTiles8)); ++t) {
-    const Tile8& c = kTiles8[t];
+  static_assert(std::size(kExactTiles) == std::size(kFastTiles), "one loop over either");
+  for (int t = 0; t < int(std::size(kFastTiles)); ++t) {
+    const Tile8& c = exact ? kExactTiles[t] : kFastTiles[t];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     for (const int want : kSplits8) {
       if (want > 1 && want * 2 > runs) break;
       const int64_t per = (runs + want - 1) / want, s = (runs + per - 1) / per;
       const double full = std::floor(double(tiles * s) / cus), rest = double(tiles * s) - full * cus;
       const double out = double(std::min<int64_t>(c.bm, M)) * double(std::min<int64_t>(c.bn, N)) *
-                         (s > 1 ? 4.0 : N % 8 ? 2.0 * c.odd : 2.0) / 17.3e6;  // one workgroup's stores
+                         (s > 1 ? 4.0 : N % 8 ? 2.0 * c.odd : 2.0) / 16.5e6;  // one workgroup's stores
       double time = full * (double(per) * c.slice + c.fixed + cus * out);
       if (rest > 0)
         time += double(per) * c.slice * (c.quiet + (1.0 - c.quiet) * rest / cus) + c.fixed + rest * out;
       time = std::max(time, mem);
-      if (s > 1) time += 5.5 + double(s) * double(M) * double(nw) * 4.0 / 4.5e6;
+      if (s > 1) time += 6.3 + double(s) * double(M) * double(nw) * 4.0 / 4.5e6;
       if (time < best_t) {
         best_t = time;
         best = {t, static_cast<int>(s), static_cast<int>(per)};
@@ -278,7 +282,7 @@ bool rows_wide(const void* p, int64_t ld, int bytes) {
 
 size_t linear_fp8_workspace_bytes(const moe_linear_fp8_desc& d) {
   if (d.rows <= kFewRows) return 0;
-  // (either output type's, so that the sizes alone decide)
+  // (either kind of sums', so that the sizes alone decide)
   const int splits = std::max(plan8(d.rows, d.cols, d.inner, false).splits,
                               plan8(d.rows, d.cols, d.inner, true).splits);
   return splits > 1 ? size_t(splits) * d.rows * ((d.cols + 7) / 8 * 8) * 4 : 0;
@@ -297,7 +301,7 @@ hipError_t launch_linear_fp8(const moe_linear_fp8_desc& d, const void* x, const 
   g.M = d.rows;
   Epilogue& e = g.e;
   e.out = y, e.bias = bias, e.res = static_cast<const uint16_t*>(residual);
-  e.ldo = d.ldy, e.ldr = d.ldr, e.act = d.act;
+  e.ldo = d.ldy, e.ldr = d.ldr, e.act = d.act & ~MOE_FP8_FAST;
   e.f16 = d.dtype == MOE_ROWS_F16, e.out_f32 = d.y_f32 != 0;
   e.vec = d.cols % 8 == 0 && rows_wide(y, d.ldy, d.y_f32 ? 4 : 2) && rows_wide(residual, d.ldr, 2);
   if (d.rows <= kFewRows) {
@@ -316,22 +320,29 @@ hipError_t launch_linear_fp8(const moe_linear_fp8_desc& d, const void* x, const 
     else go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
     return hipGetLastError();
   }
-  const Plan8 p = plan8(d.rows, d.cols, d.inner, d.y_f32 != 0);
-  const Tile8& c = kTiles8[p.tile];
+  const bool exact = !(d.act & MOE_FP8_FAST);
+  const Plan8 p = plan8(d.rows, d.cols, d.inner, exact);
+  const Tile8& c = exact ? kExactTiles[p.tile] : kFastTiles[p.tile];
   g.tiles_m = static_cast<int>((d.rows + c.bm - 1) / c.bm);
   g.tiles_n = static_cast<int>((d.cols + c.bn - 1) / c.bn);
   g.splits = p.splits, g.per_split = p.per_split;
   g.part = static_cast<float*>(ws), g.nw = (d.cols + 7) / 8 * 8;
   const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n * g.splits;
   hipError_t err;
-  switch (p.tile) {
-    case 0: err = launch8<kDense, 256, 256, 2>(g, tiles, s); break;
-    case 1: err = launch8<kDense, 128, 256, 3>(g, tiles, s); break;
-    case 2: err = launch8<kDense, 256, 128, 3>(g, tiles, s); break;
-    default:
-      err = e.out_f32 ? launch8<kDense, 128, 128, 4, true>(g, tiles, s)
-                      : launch8<kDense, 128, 128, 4>(g, tiles, s);
-      break;
+  if (exact) {
+    switch (p.tile) {
+      case 0: err = launch8<kDense, 160, 256, 2, true>(g, tiles, s); break;
+      case 1: err = launch8<kDense, 256, 128, 3, true>(g, tiles, s); break;
+      case 2: err = launch8<kDense, 128, 128, 4, true>(g, tiles, s); break;
+      default: err = launch8<kDense, 64, 256, 3, true>(g, tiles, s); break;
+    }
+  } else {
+    switch (p.tile) {
+      case 0: err = launch8<kDense, 256, 256, 2>(g, tiles, s); break;
+      case 1: err = launch8<kDense, 128, 256, 3>(g, tiles, s); break;
+      case 2: err = launch8<kDense, 256, 128, 3>(g, tiles, s); break;
+      default: err = launch8<kDense, 128, 128, 4>(g, tiles, s); break;
+    }
   }
   if (err != hipSuccess || g.splits == 1) return err;
   const int64_t threads = d.rows * (g.nw / 8);
@@ -350,7 +361,7 @@ hipError_t launch_gate_up_fp8(const moe_grouped_fp8_desc& d, const void* x, cons
   g.gather = src_row, g.top_k = d.top_k, g.tokens = d.num_tokens;
   g.h = static_cast<uint8_t*>(h), g.hs = hs;
   if (d.fast) return launch8<kGated, 256, 256, 2>(g, INT64_MAX, s);
-  return launch8<kGated, kGatedRows, 256, 2, true>(g, INT64_MAX, s);
+  return launch8<kGated, kExactRows, 256, 2, true>(g, INT64_MAX, s);
 }
 
 hipError_t launch_down_fp8(const moe_grouped_fp8_desc& d, const void* h, const float* hs,
@@ -360,7 +371,8 @@ hipError_t launch_down_fp8(const moe_grouped_fp8_desc& d, const void* h, const f
   g.offsets = offsets, g.counts = counts, g.groups = d.num_groups;
   g.m_cap = d.m_cap, g.max_rows = static_cast<int>(std::min<int64_t>(d.max_rows, INT32_MAX));
   g.e.out = y, g.e.ldo = d.cols, g.e.vec = true;
-  return launch8<kGrouped, 256, 256, 2>(g, INT64_MAX, s);
+  if (d.fast) return launch8<kGrouped, 256, 256, 2>(g, INT64_MAX, s);
+  return launch8<kGrouped, kExactRows, 256, 2, true>(g, INT64_MAX, s);
 }
 
 }  // namespace moe

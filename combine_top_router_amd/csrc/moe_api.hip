@@ -695,8 +695,8 @@ int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mat
 static int32_t linear_fp8_status(const moe_linear_fp8_desc* d) {
   constexpr int32_t kDim = 1 << 20;
   if (!d || d->rows < 0 || d->rows >= (int64_t(1) << 31) || d->inner < 1 || d->inner > kDim ||
-      d->cols < 1 || d->cols > kDim || d->act < MOE_ACT_NONE || d->act > MOE_ACT_GELU ||
-      (d->y_f32 != 0 && d->y_f32 != 1) || d->reserved || !row_stride_ok(d->ldy, d->cols))
+      d->cols < 1 || d->cols > kDim || (d->act & ~MOE_FP8_FAST) < MOE_ACT_NONE ||
+      (d->act & ~MOE_FP8_FAST) > MOE_ACT_GELU || (d->y_f32 != 0 && d->y_f32 != 1) || d->reserved || !row_stride_ok(d->ldy, d->cols))
     return MOE_ERR_ARG;
   if ((d->dtype != MOE_ROWS_BF16 && d->dtype != MOE_ROWS_F16) || d->inner % 16 ||
       !moe::linear_fp8_launchable(*d))

@@ -100,8 +100,8 @@ class MoELayer:
         norm: the gain [H] fp32 of a root-mean-square norm of the input (plus a
         residual, where the call gives one; their sum is then in ``total``), ``eps`` its
         epsilon. fp8: the weights are held in e4m3 with scales (needs ``gather``), the
-        products run on 8-bit operands; with fp8_fast gate/up sums by the 8-bit matrix
-        instruction (``ops.grouped_gate_up_fp8``)."""
+        products run on 8-bit operands; with fp8_fast their sums are the 8-bit matrix
+        instruction's (``ops.grouped_gate_up_fp8``, ``ops.linear_fp8``)."""
         if fp8 and not gather:
             raise ValueError("fp8 gathers its rows: there is no 8-bit permute")
         if fp8_fast and not fp8:
@@ -235,7 +235,8 @@ class MoELayer:
             ]
         if self.fp8:
             down = ("down", lambda: ops.grouped_down_fp8(
-                self.h, self.h_scale, L.offsets, L.local_counts, *self.w2q, self.T, self.y))
+                self.h, self.h_scale, L.offsets, L.local_counts, *self.w2q, self.T, self.y,
+                self.fp8_fast))
         else:
             down = ("down", lambda: ops.grouped_down(self.h, L.offsets, L.local_counts, self.w2t,
                                                      out=self.y))
@@ -250,7 +251,7 @@ class MoELayer:
                     h=self.shared_h[0], h_scale=self.shared_h[1], fast=self.fp8_fast)),
                 ("shared_down", lambda: ops.linear_fp8(
                     *self.shared_h, *self.shared_w2, residual=self.out, out=self.out,
-                    workspace=self.shared_ws)),
+                    workspace=self.shared_ws, fast=self.fp8_fast)),
             ]
         elif self.shared_w2 is not None:
             back += [

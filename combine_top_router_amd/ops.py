@@ -515,6 +515,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, act: str
 
 _ROWS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _F8 = torch.float8_e4m3fn
+_FP8_FAST = 32
 
 
 def _row_type(t, name: str) -> int:
@@ -683,18 +684,20 @@ def linear_fp8_workspace_bytes(x: torch.Tensor, w: torch.Tensor) -> int:
 
 def linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                bias=None, act: str = "none", residual=None, out_dtype=None, out=None,
-               workspace=None) -> torch.Tensor:
+               workspace=None, fast: bool = False) -> torch.Tensor:
     """act(x w^T + bias) + residual on 8-bit operands: x [M, K] e4m3 with x_scale
     [M, ceil(K / 128)] (quantize_fp8, rms_norm), w [N, K] e4m3 with w_scale
     [ceil(N / 128), ceil(K / 128)] (quantize_fp8_weights), bias [N] fp32, residual [M, N]
     bf16 or fp16; the result bf16 (the default), fp16 or fp32. ``out`` may be
-    ``residual``. fp32 sums, one rounding. The gradient of x is the same call on the
-    transposed weights."""
+    ``residual``. fp32 sums, one rounding. ``fast``: more than 64 rows are summed by the
+    8-bit matrix instruction, up to twice as fast, 1.4e-5 of the result's norm off on normal
+    values. The gradient of x is the same call on the transposed weights."""
     dev = x.device
     dt = out.dtype if out is not None else torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype is not None and dt != out_dtype:
         raise TypeError(f"out must be {out_dtype} (got {dt})")
     desc = _linear_fp8_desc(x, w, act, dt, None if residual is None else residual.dtype)
+    desc.act |= _FP8_FAST if fast else 0
     M, K, N = desc.rows, desc.inner, desc.cols
     _need_fp8(x, x_scale, "x", (M, K), (M, _runs(K)))
     _need_fp8(w, w_scale, "w", (N, K), (_runs(N), _runs(K)))
@@ -761,13 +764,14 @@ def grouped_gate_up_fp8(x: torch.Tensor, x_scale: torch.Tensor, offsets, counts,
 
 
 def grouped_down_fp8(h: torch.Tensor, h_scale: torch.Tensor, offsets, counts, w2, w2_scale,
-                     max_rows=None, out=None) -> torch.Tensor:
+                     max_rows=None, out=None, fast: bool = False) -> torch.Tensor:
     """y [m_cap, H] bf16 = h W2 per local expert group, on 8-bit h [m_cap, I] with h_scale
     [m_cap, I / 128] and w2 [E_loc, H, I] with w2_scale [E_loc, H / 128, I / 128];
-    ``max_rows`` as in grouped_gate_up_fp8."""
+    ``max_rows`` and ``fast`` as in grouped_gate_up_fp8."""
     dev = h.device
     m_cap = h.shape[0]
     desc, n, I, H = _grouped_fp8(h, offsets, counts, w2, m_cap, max_rows, "w2")
+    desc.fast = bool(fast)
     _need_fp8(h, h_scale, "h", (m_cap, I), (m_cap, _runs(I)))
     _need_fp8(w2, w2_scale, "w2", (n, H, I), (n, _runs(H), _runs(I)))
     out = _out(out, "y", torch.bfloat16, (m_cap, H), dev)

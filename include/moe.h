@@ -629,10 +629,11 @@ int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mat
  *             + bias[n]
  *   y = act(z) + residual      fp32, rounded once to y's type
  *
- * The products of a run are summed on the matrix cores, the runs in fp32. An fp32 y, and any y of at
- * most 64 rows, has 24-bit sums throughout; a 16-bit y of more rows comes from the 8-bit matrix
- * instruction, which cuts each of 8 neighbouring products to a multiple of 2^-13 of the largest
- * one's power of two before it adds them (1.4e-5 of y's norm on normal values, unbiased). act as in moe_linear.
+ * The products of a run are summed on the matrix cores, the runs in fp32, with 24 bits throughout.
+ * With act | MOE_FP8_FAST, more than 64 rows are summed by the 8-bit matrix instruction, up to twice as
+ * fast, which cuts each of 8 neighbouring products to a multiple of 2^-13 of the largest one's power of two
+ * before it adds them: 1.4e-5 of y's norm on normal values, and more where large products
+ * cancel. act as in moe_linear.
  * The gradient of x is the same product with the transposed weights: blocks of 128 x 128
  * keep their values when turned over (moe_quantize_fp8_weights with the other w_order).
  *   x_d         [rows, inner] e4m3, dense;  x_scale_d [rows, ceil(inner / 128)] float
@@ -647,12 +648,14 @@ int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mat
  *   workspace_d >= moe_linear_fp8_workspace_bytes(desc) bytes, 16-byte aligned (NULL if that
  *   is 0); contents on entry do not matter. Calls that may overlap need workspaces of their own.
  */
+enum { MOE_FP8_FAST = 32 }; /* with act: moe_linear_fp8's sums by the 8-bit matrix instruction */
+
 typedef struct moe_linear_fp8_desc {
   int64_t rows;  /* M */
   int32_t inner; /* K */
   int32_t cols;  /* N */
   int32_t dtype; /* MOE_ROWS_BF16 or MOE_ROWS_F16: of y (unless y_f32) and the residual */
-  int32_t act;   /* MOE_ACT_* */
+  int32_t act;   /* MOE_ACT_*, or with MOE_FP8_FAST */
   int32_t y_f32; /* 0 or 1 */
   int32_t reserved; /* 0 */
   int64_t ldy, ldr;
@@ -674,9 +677,9 @@ int32_t moe_linear_fp8(const moe_linear_fp8_desc* desc, const void* x_d, const f
  *                             128 columns of a row, as moe_quantize_fp8 takes it
  *   moe_grouped_down_fp8:     y = h W2[e], rounded once to bf16
  *
- * Sums as in moe_linear_fp8: gate_up's at full width, since a scale is an fp32 output; with `fast`
- * by the 8-bit instruction, for up to 1.8 times the speed with many rows to a group, and scales
- * 1.2e-5 off. Rows outside the groups are neither read nor written.
+ * Sums with 24 bits throughout; with `fast` by the 8-bit instruction (moe_linear_fp8), whatever the rows, up
+ * to 1.8 times as fast with many rows to a group, gate_up's scales 1.2e-5 off. Rows outside the groups are
+ * neither read nor written.
  *   x_d        [m_cap, inner] e4m3, or with src_row_d [num_tokens, inner]: row r of the groups is then
  *              x[src_row[r] / top_k] (moe_layout's src_row); a row whose src_row is not of [0, num_tokens top_k)
  *              holds no defined values
@@ -700,7 +703,7 @@ typedef struct moe_grouped_fp8_desc {
   int32_t inner;
   int32_t cols;
   int32_t top_k; /* with src_row_d */
-  int32_t fast;  /* gate_up: 0 or 1, see there */
+  int32_t fast;  /* 0 or 1 */
   int32_t reserved; /* 0 */
 } moe_grouped_fp8_desc;
 
