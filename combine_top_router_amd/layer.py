@@ -108,6 +108,9 @@ class MoELayer:
             raise ValueError("fp8_fast needs fp8")
         if fp8 and (hidden % 128 or inter % 128):
             raise ValueError(f"fp8 needs multiples of 128 (got hidden {hidden}, inter {inter})")
+        if fp8 and num_tokens * hidden >= 1 << 31:
+            raise ValueError(f"fp8 gathers its rows from less than 2 GiB: at most "
+                             f"{((1 << 31) - 1) // hidden} tokens of {hidden} (got {num_tokens})")
         if shared is not None and ep_size > 1 and local_rank >= 0:
             raise ValueError("a rank's share of the experts takes no shared expert: the sum over "
                              "the ranks would count it on each of them")
@@ -118,6 +121,8 @@ class MoELayer:
             _check_router(router, num_experts, top_k, dev)
         if norm is not None:
             _check(norm, "norm", torch.float32, (hidden,), dev)
+            if hidden % 8 or not 8 <= hidden <= 16384:
+                raise ValueError(f"norm needs a hidden size that is a multiple of 8, up to 16384 (got {hidden})")
             if not (math.isfinite(eps) and eps >= 0):
                 raise ValueError(f"eps must be finite and not negative (got {eps})")
         if shared is not None:

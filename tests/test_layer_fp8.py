@@ -41,3 +41,16 @@ def test_fp8():
     s = torch.zeros((128, 64), dtype=BF)
     with pytest.raises(ValueError, match="multiples of 128"):
         _layer(fp8=True, shared=(s, s, s.t().contiguous()))
+
+
+@pytest.mark.parametrize("hidden", [16392, 20, 4])
+def test_norm_of_a_width_that_its_call_refuses(hidden):
+    with pytest.raises(ValueError, match="norm needs a hidden size"):
+        _layer(H=hidden, norm=torch.ones(hidden))
+
+
+@pytest.mark.parametrize("tokens,hidden", [(1 << 24, 128), (1 << 23, 256), ((1 << 31) // 384 + 1, 384)])
+def test_fp8_of_more_rows_than_its_gather_reaches(tokens, hidden):
+    w = torch.zeros((1, hidden, 128), dtype=BF)
+    with pytest.raises(ValueError, match="tokens"):
+        MoELayer(tokens, hidden, 1, 1, 128, w, w, torch.zeros((1, 128, hidden), dtype=BF), fp8=True)
