@@ -733,7 +733,7 @@ static int32_t grouped_fp8_status(const moe_grouped_fp8_desc* d, bool gather, in
     return MOE_ERR_ARG;
   if (gather && (d->num_tokens < 0 || d->top_k < 1 || d->top_k > kMaxTopK)) return MOE_ERR_ARG;
   if (d->inner % 128 || d->cols % 128 || d->m_cap >= (int64_t(1) << 31) ||
-      (gather && d->num_tokens >= (int64_t(1) << 31) / d->inner) ||
+      (gather && d->num_tokens > ((int64_t(1) << 31) - 1) / d->inner) ||
       (d->m_cap / 65 + d->num_groups) * ((d->cols + tile - 1) / tile) >= (int64_t(1) << 30))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

@@ -69,3 +69,16 @@ def test_down_takes_the_flag_and_nothing_else():
     for fast, status in ((0, 0), (1, 0), (2, 1), (-1, 1)):
         d = _lib.GroupedFp8Desc(m_cap=0, max_rows=1, num_groups=1, inner=128, cols=128, fast=fast)
         assert lib.moe_grouped_down_fp8(C.byref(d), *p, None) == status
+
+
+@built
+def test_gathered_rows_up_to_the_stated_limit():
+    """num_tokens * inner < 2^31, also where inner is no power of two."""
+    from combine_top_router_amd import _lib
+    lib = _lib.load()
+    p = [C.c_void_p((i + 1) << 20) for i in range(11)]  # never dereferenced
+    for inner in (128, 384, 7168):
+        most = ((1 << 31) - 1) // inner
+        for tokens, status in ((most, 0), (most + 1, 2)):
+            d = _lib.GroupedFp8Desc(m_cap=0, max_rows=1, num_tokens=tokens, num_groups=1, inner=inner, cols=128, top_k=1)
+            assert lib.moe_grouped_gate_up_fp8(C.byref(d), *p, None) == status, (inner, tokens)
