@@ -4,6 +4,7 @@
 
 #include "fp8.h"
 #include "linear_epilogue.h"
+#include "row_tiles.h"
 #include "slice_range.h"
 
 namespace moe {
@@ -854,11 +855,9 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
       const int64_t room = o < 0 ? 0 : max(int64_t(0), g.m_cap - o);
       const int c = int(min(int64_t(min(max(g.counts[e], 0), g.max_rows)), room));
       groups.cnt[e] = c, groups.off[e] = o;
-      tiles += (c + BM - 1) / BM;
-      if constexpr (FEW > 0) few += min((c + FEW - 1) / FEW, 1 << 16);
+      if constexpr (FEW > 0) tiles += choice_tiles(c, BM), few += choice_tiles(c, FEW);
     }
     if constexpr (FEW > 0) {
-      tiles = min(tiles, 1 << 16);
 #pragma unroll
       for (int off = 1; off < kWave; off <<= 1)
         tiles += __shfl_xor(tiles, off, kWave), few += __shfl_xor(few, off, kWave);
@@ -869,7 +868,7 @@ __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
 #pragma unroll
       for (int w = 0; w < kWaves8; ++w) tiles += groups.wave[w], few += groups.wave[kWaves8 + w];
       __syncthreads();
-      if (uniform(few) * 4 <= uniform(tiles) * (KIND == kGated || EXACT ? 5 : 8))
+      if (takes_small(uniform(few), uniform(tiles), KIND == kGated || EXACT ? 5 : 8))
         return fp8_tiles<FEW, BN, 3, KIND, WIDE, EXACT>(g, smem, groups, amax_s);
     }
   }

@@ -5,11 +5,7 @@
 
 #include <cstdint>
 
-#ifdef __HIP__
-#define MOE_HOST_DEVICE __host__ __device__
-#else
-#define MOE_HOST_DEVICE
-#endif
+#include "host_device.h"
 
 namespace moe {
 
