@@ -641,10 +641,10 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
       const bool parts = KIND == kDense && g.splits > 1;
       const int64_t nw = t.n0 + wn * 64;
       // Nothing to do but to add a residual, to round and to store: without the general form's
-      // vector work, which took a third of a tile's time at six runs (65536x768x2048: 157 -> 133 us, now 129).
+      // vector work, which took a third of a tile's time at six runs (65536x768x2048, fast: 157 -> 133 us, now 128).
       // Two neighbouring lanes' rows change halves, so that a store, and a load of the residual, takes
-      // 128 bytes of a row and not 64: first the even rows, then the odd ones (65536x2048x7168: 961 -> 919 us,
-      // with a residual 1152 -> 1080).
+      // 128 bytes of a row and not 64: first the even rows, then the odd ones (65536x2048x7168, fast: 961 -> 910 us,
+      // with a residual 1152 -> 1085).
       auto store_rows = [&](auto res_tag) __attribute__((always_inline)) {
         constexpr bool RES = decltype(res_tag)::value;
         const bool odd = r15 & 1;
@@ -836,6 +836,8 @@ __device__ __forceinline__ void fp8_tiles(const Fp8Args g, char* const smem, Gro
 // 232 -> 288; skewed groups' gate/up with 1.22 times the tiles 223 -> 208, with 1.47 times 204 -> 227. fast,
 // 256 rows against 64: groups of 32 203 -> 162 and 114 -> 98, of 100 (twice) 215 -> 225 and 122 -> 119, of
 // 160 (three times) 214 -> 311 and 122 -> 172. So up to 5/4 times the tiles, and fast's down up to twice.
+// (Where the large tile is taken it is as fast as in a kernel without the small one: groups of 256 to 2048 rows
+// and skewed ones within 2 %, fast's gate/up 2 to 7 % faster.)
 template <int BM, int BN, int NS, int KIND, bool WIDE, bool EXACT, int FEW>
 __global__ __launch_bounds__(kThreads8, 1) void fp8_kernel(Fp8Args g) {
   constexpr bool RAGGED = KIND != kDense;

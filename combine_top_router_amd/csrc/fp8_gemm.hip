@@ -3,9 +3,9 @@
 //   z[m, n] = sum over runs b of sa[m, b] sw[n / 128, b] p_b[m, n],
 //   p_b[m, n] = sum over k in [128 b, 128 b + 128) of a[m, k] w[n, k]
 //
-// A run is as long as one 16x16x128 instruction: its sum starts from zero, is scaled by an fp32
-// factor of its row and its block of columns and added in fp32, so that each product costs one matrix
-// instruction and four vector additions for 16 x 16 outputs. Both operands lie with k last,
+// A run is as long as one 16x16x128 instruction, or four of 16x16x32: its sum starts from zero, is scaled by
+// an fp32 factor of its row and its block of columns and added in fp32, so that each product costs its matrix
+// instructions and four vector additions for 16 x 16 outputs. Both operands lie with k last,
 // w output-major; the product is taken as w a^T, which leaves four neighbouring columns of a row
 // in a lane and 16-byte stores.
 //
@@ -22,14 +22,14 @@
 // Two ways to a run's sum (run_product_exact, run_product): fp16 copies of the values, whose sums keep
 // 24 bits; and where the caller asks for it (fast) the 8-bit instruction, at twice the rate, which loses 1.4e-5.
 //
-// Bound, with many rows: the matrix cores and their clock (1.7 to 1.9 GHz under this load). 8192x8192x8192
-// takes 435 us, 2530 TFLOP/s; a product with one scale for all, which needs no vector work,
-// reaches 2816 on the same card. Beside a product about five vector instructions are free, the
-// scaled addition and its scale take five: a sixth cost a fifth of the time. 65536x2048x7168
-// (few slices to a tile): 919 us, 2090 TFLOP/s, and with a residual 1080: its loads come
-// between the stores of 128 KB a tile.
-// Few rows: one read of w. 16x7168x4096: 10.2 us, 2.9 TB/s; 32 experts' gate/up, 7168 -> 2048,
-// 32 rows each: 168 us, 5.6 TB/s; down 104 us, 4.5 TB/s.
+// Bound, with many rows: the matrix cores and their clock (1.7 to 2.1 GHz under this load), beside them the
+// conversions to fp16. 8192x8192x8192 takes 917 us, 1200 TFLOP/s (a bf16 product of that size 1393);
+// 65536x2048x7168 (few slices to a tile) 1660 us, and with a residual 1830: its loads come
+// between the stores of a tile. fast: 452 us, 2430 TFLOP/s (a product with one scale for all, which
+// needs no vector work, 2776), 910 and 1085 us; beside a product about five vector instructions are free
+// there, the scaled addition and its scale take five: a sixth cost a fifth of the time.
+// Few rows: one read of w. 16x7168x4096: 8.0 us, 3.7 TB/s; 32 experts' gate/up, 7168 -> 2048,
+// 32 rows each: 167 us, 5.6 TB/s; down 103 us, 4.6 TB/s.
 #include <algorithm>
 
 #include "fp8_gemm.h"
@@ -39,7 +39,7 @@ namespace moe {
 namespace {
 
 // Few rows (16 RB at most): bound by reading w once, and of a single call by the time that a
-// chip full of first loads takes (16x7168x4096: 10.2 us, 29 MB). A workgroup takes 16 CB columns, its
+// chip full of first loads takes (16x7168x4096: 8.0 us, 29 MB). A workgroup takes 16 CB columns, its
 // WAVES wavefronts an equal share of the runs each, through a ring of D runs in LDS that is
 // the wavefront's own: no barrier until the wavefronts' sums meet in LDS at the end. (Fragments
 // read from memory as they are needed, 16 rows x 64 bytes each, took half as long again:
@@ -251,7 +251,7 @@ hipError_t launch_linear_fp8(const moe_linear_fp8_desc& d, const void* x, const 
   e.vec = d.cols % 8 == 0 && rows_wide(y, d.ldy, d.y_f32 ? 4 : 2) && rows_wide(residual, d.ldr, 2);
   if (d.rows <= kFewRows) {
     // 32 columns to a workgroup halve what is read of x, where that leaves enough of them
-    // (16x7168x7168: 15.1 us, with 16 columns 17.6; 16x7168x4096: 12.3 and 10.3)
+    // (with the host's side, 16x7168x7168: 15.1 us, with 16 columns 17.6; 16x7168x4096: 12.3 and 10.3)
     auto go = [&](auto rb, auto depth) {
       constexpr int RB = decltype(rb)::value, D = decltype(depth)::value, W = kWaves8;
       if (d.cols >= 24 * device_cu_count())

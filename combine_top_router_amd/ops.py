@@ -740,7 +740,7 @@ def grouped_gate_up_fp8(x: torch.Tensor, x_scale: torch.Tensor, offsets, counts,
     with ``transpose`` of the math orientation). Rows of a group past ``max_rows`` (the
     token count, say) are not computed; rows outside the groups not written. ``fast``: sums by
     the 8-bit matrix instruction, up to 1.8 times as fast with many rows to a group, the
-    scales 1.2e-5 off."""
+    scales up to 2e-5 off (root mean square)."""
     dev = x.device
     gather = src_row is not None
     if gather:

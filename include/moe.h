@@ -549,8 +549,8 @@ int32_t moe_linear_backward(const moe_linear_desc* desc, const void* dy_d, const
  *   q_d         [rows, hidden] e4m3, dense, or NULL (out); scale_d [rows, ceil(hidden / 128)]
  *               float, with q_d (out)
  * total and y may each be x or the residual (same address and stride), not both the same one; other
- * buffers must not overlap. A row whose sum of squares is past fp32's range gets rstd = 0, a NaN
- * reaches its row alone. rows = 0 is a no-op.
+ * buffers must not overlap. A row whose sum of squares is past fp32's range gets rstd = 0, one whose squares
+ * vanish (all below about 1e-23) with eps = 0 an infinite rstd; a NaN reaches its row alone. rows = 0 is a no-op.
  * Limits: 0 <= rows < 2^31, hidden a multiple of 8, 8 <= hidden <= 16384, eps >= 0 and finite,
  * dtype MOE_ROWS_*, strides multiples of 8 from hidden to 2^21, all buffers 16-byte aligned.
  */
@@ -644,7 +644,7 @@ int32_t moe_quantize_fp8_weights(int32_t dtype, const void* w_d, int32_t num_mat
  * y may be the residual itself (same address, stride and type); other buffers must not overlap.
  * Limits: 0 <= rows < 2^31, inner a multiple of 16 from 16 to 2^20, 1 <= cols <= 2^20; dtype
  * MOE_ROWS_BF16 or MOE_ROWS_F16; ldy and (read only with its buffer) ldr from cols to 2^21; fewer than 2^26
- * tiles of 128 x 128 outputs and 2^35 outputs (else MOE_ERR_UNSUPPORTED). x_d and w_d 16-byte aligned.
+ * tiles of 128 x 128 outputs and 2^32 - 64 pieces of 8 columns of a row (else MOE_ERR_UNSUPPORTED). x_d and w_d 16-byte aligned.
  *   workspace_d >= moe_linear_fp8_workspace_bytes(desc) bytes, 16-byte aligned (NULL if that
  *   is 0); contents on entry do not matter. Calls that may overlap need workspaces of their own.
  */
@@ -678,7 +678,7 @@ int32_t moe_linear_fp8(const moe_linear_fp8_desc* desc, const void* x_d, const f
  *   moe_grouped_down_fp8:     y = h W2[e], rounded once to bf16
  *
  * Sums with 24 bits throughout; with `fast` by the 8-bit instruction (moe_linear_fp8), whatever the rows, up
- * to 1.8 times as fast with many rows to a group, gate_up's scales 1.2e-5 off. Rows outside the groups are
+ * to 1.8 times as fast with many rows to a group, gate_up's scales up to 2e-5 off (root mean square). Rows outside the groups are
  * neither read nor written.
  *   x_d        [m_cap, inner] e4m3, or with src_row_d [num_tokens, inner]: row r of the groups is then
  *              x[src_row[r] / top_k] (moe_layout's src_row); a row whose src_row is not of [0, num_tokens top_k)
